@@ -1,7 +1,7 @@
 /*
  * dq.h — C ABI of the B200 (sm_100a) per-token dynamic quantization library.
  *
- * Five operations, launched asynchronously on the caller's stream:
+ * Eight operations, launched asynchronously on the caller's stream:
  *
  *   dq_dynamic_quant        aclnnDynamicQuantV2, "Formula" and "Description":
  *                           per-row (per-token) symmetric or asymmetric
@@ -20,10 +20,19 @@
  *   dq_w8a8_gemm            aclnnQuantBatchMatmulInplaceAdd: the consumer of
  *                           the codes, a W8A8 product with per-token x
  *                           per-channel scales on the tensor cores.
+ *   dq_w8a8_linear          the same product with bias, activation and
+ *                           residual in its epilogue.
+ *   dq_qk_norm_rope         RMS norm of every query and key head with the
+ *                           position rotation in the same pass
+ *                           (dq_qk_norm_rope_cache: keys and values go
+ *                           straight into a paged 16-bit or INT8 cache).
+ *   dq_paged_attention      attention of one new token per sequence over
+ *                           that cache, split over its length and joined.
  *
  * plus the workspace queries of the two-phase calling convention both pages
- * describe ("...GetWorkspaceSize" first, then the run): dq_get_workspace_size
- * and dq_ada_layernorm_quant_get_workspace_size.
+ * describe ("...GetWorkspaceSize" first, then the run): dq_get_workspace_size,
+ * dq_ada_layernorm_quant_get_workspace_size and
+ * dq_paged_attention_get_workspace_size.
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer (cudaMalloc'd or equivalent),
@@ -295,6 +304,164 @@ dq_status dq_dequant_per_group(const void* y, dq_dtype y_dtype, int64_t rows, in
 dq_status dq_w8a8_gemm(const int8_t* a, const int8_t* b, int64_t m, int64_t n, int64_t k,
                        const float* a_scale, const float* b_scale, void* out, dq_dtype out_dtype,
                        int32_t accumulate, cudaStream_t stream);
+
+/* Activation of dq_w8a8_linear's epilogue. GELU is 0.5 x (1 + erf(x / sqrt 2));
+ * GELU_TANH 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))); SILU
+ * x / (1 + exp(-x)). */
+typedef enum dq_activation {
+  DQ_ACT_NONE = 0,
+  DQ_ACT_RELU = 1,
+  DQ_ACT_GELU = 2,
+  DQ_ACT_GELU_TANH = 3,
+  DQ_ACT_SILU = 4
+} dq_activation;
+
+/* W8A8 linear layer: dq_w8a8_gemm's product with bias, activation and
+ * residual applied before the result leaves the chip:
+ *   t[m,n]   = float(sum_k a[m,k] * b[n,k]) * (a_scale[m] * b_scale[n])
+ *   t[m,n]  += bias[n]                         (when bias != NULL)
+ *   t[m,n]   = activation(t[m,n])
+ *   t[m,n]  += residual[m,n]                   (when residual != NULL)
+ *   out[m,n] = t[m,n] rounded to out_dtype
+ * The integer sum is exact; everything after it is binary32, the products and
+ * sums rounded once in that order (without an activation the result is
+ * therefore bit-identical to the formula); the activations' exponentials and
+ * error function are accurate to a few units in the last place of binary32.
+ * Arguments: a, b, m, n, k, a_scale, b_scale as in dq_w8a8_gemm;
+ *   bias        device [n] of bias_dtype (DQ_F32, DQ_F16, DQ_BF16) or NULL
+ *               (bias_dtype then ignored).
+ *   activation  a dq_activation.
+ *   residual    device [m, n] of out_dtype, or NULL. It may be `out` itself
+ *               (the residual stream updated in place); it must not overlap
+ *               `out` in any other way.
+ *   out         device [m, n] of out_dtype (DQ_F32, DQ_F16, DQ_BF16).
+ * m == 0 or n == 0 is a no-op. Calls of few tokens read the weights with all
+ * SMs, K split over the CTAs of a cluster and the exact integer parts joined
+ * through its shared memory, so the result does not depend on the split.
+ * Errors: as dq_w8a8_gemm (DQ_ERR_BAD_ARGUMENT for an unknown activation). */
+dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m, int64_t n, int64_t k,
+                         const float* a_scale, const float* b_scale, const void* bias, dq_dtype bias_dtype,
+                         dq_activation activation, const void* residual, void* out, dq_dtype out_dtype,
+                         cudaStream_t stream);
+
+/* Largest head dimension of the head-wise operators below. */
+#define DQ_MAX_HEAD_DIM 256
+/* Largest number of query heads, and of key heads, of those operators. */
+#define DQ_MAX_HEADS 1024
+
+/* RMS norm of every query and key head and the rotation by the token's
+ * position, in one pass. For every token t and head row x [head_dim] of q
+ * (weight w = q_weight) and of k (w = k_weight):
+ *   y[c] = x[c] / sqrt(mean_c(x[c]^2) + epsilon) * w[c]
+ *   angle_i = positions[t] * inv_freq[i]             i < rope_dim / 2
+ *   (y[a], y[b]) <- (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
+ * with (a, b) = (i, i + rope_dim / 2), or (2i, 2i + 1) when interleaved;
+ * channels from rope_dim on are normed only. Norm and rotation are binary32,
+ * rounded once into the output; the angle is reduced in binary64, so far
+ * positions keep their accuracy (any int32 position is valid).
+ * Arguments
+ *   q, k         device, token t's heads at q + t * q_stride (elements), head
+ *                h of it at + h * head_dim: slices of one fused projection
+ *                work as they are. q_stride >= q_heads * head_dim, k_stride >=
+ *                kv_heads * head_dim. DQ_F16 or DQ_BF16 (both, and the
+ *                outputs, of `dtype`).
+ *   q_weight, k_weight  device [head_dim] of weight_dtype (DQ_F32, DQ_F16,
+ *                DQ_BF16), or NULL for 1.
+ *   epsilon      finite, >= 0.
+ *   positions    device int32 [tokens].
+ *   inv_freq     device float [rope_dim / 2]; NULL only with rope_dim 0.
+ *   rope_dim     even, 0 <= rope_dim <= head_dim.
+ *   interleaved  0 or 1.
+ *   q_out, k_out device, strided as q and k are. q_out may be q itself with
+ *                the same stride, k_out may be k likewise.
+ * 1 <= head_dim <= DQ_MAX_HEAD_DIM; 1 <= q_heads, kv_heads <= DQ_MAX_HEADS;
+ * 0 <= tokens < 2^31, and 0 is a no-op. Rows of 16-byte aligned vectors take
+ * a vectorised path; others a scalar one, with the same formula. A row's
+ * value never depends on the other rows, or on how many there are.
+ * Errors: DQ_ERR_BAD_SHAPE, DQ_ERR_BAD_DTYPE, DQ_ERR_BAD_ARGUMENT,
+ * DQ_ERR_NULL_POINTER, DQ_ERR_MISALIGNED, DQ_ERR_CUDA. */
+dq_status dq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, dq_dtype dtype,
+                          int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                          const void* q_weight, const void* k_weight, dq_dtype weight_dtype, float epsilon,
+                          const int32_t* positions, const float* inv_freq, int32_t rope_dim, int32_t interleaved,
+                          void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                          cudaStream_t stream);
+
+/* dq_qk_norm_rope with the keys, and the values as they are, written into a
+ * paged cache instead of k_out:
+ *   k_cache, v_cache  device [num_pages, kv_heads, page_size, head_dim] of
+ *                cache_dtype: `dtype`, or DQ_INT8 with the symmetric codes of
+ *                dq_dynamic_quant over each head row (scale = absmax / 127,
+ *                code = round(y / scale) of the binary32 row).
+ *   k_scale, v_scale  device float [num_pages, kv_heads, page_size], required
+ *                for DQ_INT8, otherwise ignored.
+ *   v            device, like k (v_stride).
+ *   slots        device int64 [tokens]: token t goes to row slots[t] %
+ *                page_size of page slots[t] / page_size. A slot that is
+ *                negative (padding) or >= num_pages * page_size writes nothing;
+ *                the slots of one call must otherwise differ.
+ * Only the named rows of the cache are written. q_out as in dq_qk_norm_rope;
+ * the cache must not overlap q, k or v. num_pages >= 1, page_size >= 1, both
+ * < 2^31. Errors as dq_qk_norm_rope. */
+dq_status dq_qk_norm_rope_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, dq_dtype dtype, int64_t tokens, int32_t q_heads,
+                                int32_t kv_heads, int32_t head_dim, const void* q_weight, const void* k_weight,
+                                dq_dtype weight_dtype, float epsilon, const int32_t* positions,
+                                const float* inv_freq, int32_t rope_dim, int32_t interleaved, void* q_out,
+                                int64_t q_out_stride, void* k_cache, void* v_cache, dq_dtype cache_dtype,
+                                float* k_scale, float* v_scale, const int64_t* slots, int64_t num_pages,
+                                int32_t page_size, cudaStream_t stream);
+
+/* Workspace query of dq_paged_attention: the bytes of device workspace for
+ * the parts of sequences that several CTAs share. It depends on the current
+ * device's SM count and the heads, not on the lengths. Host only.
+ * Errors: DQ_ERR_NULL_POINTER, DQ_ERR_BAD_SHAPE, DQ_ERR_BAD_DTYPE. */
+dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                                dq_dtype cache_dtype, size_t* workspace_bytes);
+
+/* Attention of one new token per sequence over a paged key-value cache (that
+ * token's own key and value already in it):
+ *   s_j = softmax_scale * sum_c q[b,h,c] * K[j,c]    for the visible tokens j
+ *   out[b,h,:] = sum_j exp(s_j) * V[j,:] / sum_j exp(s_j)
+ * Token j of sequence b, 0 <= j < lengths[b], lies in row j % page_size of
+ * page page_table[b, j / page_size]; query head h reads key head
+ * h / (q_heads / kv_heads). With DQ_INT8 caches K[j,c] = code * k_scale[j].
+ * Visible are all cached tokens when window is 0, else the last `window` of
+ * them and the first `sinks`.
+ * Arguments
+ *   q            device, sequence b's heads at q + b * q_stride (elements),
+ *                [q_heads, head_dim] each, DQ_F16 or DQ_BF16.
+ *   k_cache, v_cache, k_scale, v_scale, cache_dtype  as dq_qk_norm_rope_cache
+ *                writes them: cache_dtype is q_dtype or DQ_INT8.
+ *   page_table   device int32 [batch, max_pages]; entries past a sequence's
+ *                last page are not read.
+ *   lengths      device int32 [batch]. A sequence of length <= 0 gives zeros
+ *                (lse: -infinity) and reads no page.
+ *   window, sinks  >= 0.
+ *   softmax_scale  finite.
+ *   out          device [batch, q_heads, head_dim] of q_dtype, dense.
+ *   lse          device float [batch, q_heads] or NULL: log sum_j exp(s_j).
+ *   workspace    device, 16-byte aligned, at least the bytes queried; scratch
+ *                that needs no clearing. Calls that run concurrently need
+ *                separate workspaces.
+ * A visible token whose page_table entry lies outside [0, num_pages), or a
+ * length above max_pages * page_size, makes that sequence's rows NaN (nothing
+ * outside the cache is read). Rows of the cache that no visible token names are
+ * not read: they may hold anything. Sums and softmax statistics are
+ * binary32; for INT8 caches the weight of a token is rounded to 11 bits
+ * before it meets its codes, for 16-bit caches to the cache's precision.
+ * 1 <= head_dim <= DQ_MAX_HEAD_DIM; q_heads a multiple of kv_heads, both <=
+ * DQ_MAX_HEADS; 0 <= batch <= 65535 * 16, and 0 is a no-op; num_pages,
+ * page_size, max_pages in [1, 2^31). Head dimensions 64, 128 and 256 with
+ * 16-byte aligned tensors run on the tensor cores; others run a CUDA-core
+ * kernel (binary32 weights).
+ * Errors: as dq_qk_norm_rope, DQ_ERR_WORKSPACE_TOO_SMALL. */
+dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t q_stride, const void* k_cache,
+                             const void* v_cache, dq_dtype cache_dtype, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, const int32_t* lengths, int64_t batch, int32_t q_heads,
+                             int32_t kv_heads, int32_t head_dim, int64_t num_pages, int32_t page_size,
+                             int64_t max_pages, int64_t window, int64_t sinks, float softmax_scale, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
 /* Largest batch * hidden that dq_ada_layernorm_quant_noalloc accepts (its
  * fixed table holds this many 8-byte entries: 1 MiB per device). */

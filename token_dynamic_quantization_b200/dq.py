@@ -14,6 +14,7 @@ missing; there is no fallback path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -43,6 +44,9 @@ DQ_WS_ROWS_PAST_LAST_GROUP = 0x1
 DQ_WS_GROUP_INDEX_INVALID = 0x2
 DQ_MAX_GROUPS = 1024
 DQ_ADA_NOALLOC_MAX_TABLE = 131072
+DQ_ACT_NONE, DQ_ACT_RELU, DQ_ACT_GELU, DQ_ACT_GELU_TANH, DQ_ACT_SILU = 0, 1, 2, 3, 4
+DQ_MAX_HEAD_DIM = 256
+DQ_MAX_HEADS = 1024
 
 _vp, _i64, _i32, _f32, _sz, _ci = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
                                    ctypes.c_size_t, ctypes.c_int)
@@ -68,6 +72,20 @@ _lib.dq_w8a8_gemm.restype = _ci
 _lib.dq_ada_layernorm_quant_noalloc.argtypes = [_vp, _ci, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _ci, _f32, _vp,
                                                 _vp, _vp]
 _lib.dq_ada_layernorm_quant_noalloc.restype = _ci
+_lib.dq_w8a8_linear.argtypes = [_vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _ci, _ci, _vp, _vp, _ci, _vp]
+_lib.dq_w8a8_linear.restype = _ci
+_lib.dq_qk_norm_rope.argtypes = [_vp, _i64, _vp, _i64, _ci, _i64, _i32, _i32, _i32, _vp, _vp, _ci, _f32, _vp, _vp,
+                                 _i32, _i32, _vp, _i64, _vp, _i64, _vp]
+_lib.dq_qk_norm_rope.restype = _ci
+_lib.dq_qk_norm_rope_cache.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _ci, _i64, _i32, _i32, _i32, _vp, _vp, _ci,
+                                       _f32, _vp, _vp, _i32, _i32, _vp, _i64, _vp, _vp, _ci, _vp, _vp, _vp, _i64,
+                                       _i32, _vp]
+_lib.dq_qk_norm_rope_cache.restype = _ci
+_lib.dq_paged_attention_get_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _ci, ctypes.POINTER(_sz)]
+_lib.dq_paged_attention_get_workspace_size.restype = _ci
+_lib.dq_paged_attention.argtypes = [_vp, _ci, _i64, _vp, _vp, _ci, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i64,
+                                    _i32, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _sz, _vp]
+_lib.dq_paged_attention.restype = _ci
 
 LIBRARY_PATH = _LIB_PATH
 
@@ -140,6 +158,52 @@ def dq_ada_layernorm_quant_noalloc(x, x_dtype, batch, seq, hidden, ada_scale, ad
                                                smooth, param_dtype, epsilon, out, quant_scale, stream)
 
 
+def dq_w8a8_linear(a, b, m, n, k, a_scale, b_scale, bias, bias_dtype, activation, residual, out, out_dtype,
+                   stream) -> int:
+    """Raw call: pointers are ints (0/None for NULL). Returns the dq_status."""
+    return _lib.dq_w8a8_linear(a, b, m, n, k, a_scale, b_scale, bias, bias_dtype, activation, residual, out,
+                               out_dtype, stream)
+
+
+def dq_qk_norm_rope(q, q_stride, k, k_stride, dtype, tokens, q_heads, kv_heads, head_dim, q_weight, k_weight,
+                    weight_dtype, epsilon, positions, inv_freq, rope_dim, interleaved, q_out, q_out_stride, k_out,
+                    k_out_stride, stream) -> int:
+    """Raw call: pointers are ints (0/None for NULL). Returns the dq_status."""
+    return _lib.dq_qk_norm_rope(q, q_stride, k, k_stride, dtype, tokens, q_heads, kv_heads, head_dim, q_weight,
+                                k_weight, weight_dtype, epsilon, positions, inv_freq, rope_dim, interleaved, q_out,
+                                q_out_stride, k_out, k_out_stride, stream)
+
+
+def dq_qk_norm_rope_cache(q, q_stride, k, k_stride, v, v_stride, dtype, tokens, q_heads, kv_heads, head_dim, q_weight,
+                          k_weight, weight_dtype, epsilon, positions, inv_freq, rope_dim, interleaved, q_out,
+                          q_out_stride, k_cache, v_cache, cache_dtype, k_scale, v_scale, slots, num_pages, page_size,
+                          stream) -> int:
+    """Raw call: pointers are ints (0/None for NULL). Returns the dq_status."""
+    return _lib.dq_qk_norm_rope_cache(q, q_stride, k, k_stride, v, v_stride, dtype, tokens, q_heads, kv_heads,
+                                      head_dim, q_weight, k_weight, weight_dtype, epsilon, positions, inv_freq,
+                                      rope_dim, interleaved, q_out, q_out_stride, k_cache, v_cache, cache_dtype,
+                                      k_scale, v_scale, slots, num_pages, page_size, stream)
+
+
+def dq_paged_attention_get_workspace_size(batch: int, q_heads: int, kv_heads: int, head_dim: int,
+                                          cache_dtype: int) -> int:
+    out = _sz(0)
+    st = _lib.dq_paged_attention_get_workspace_size(batch, q_heads, kv_heads, head_dim, cache_dtype,
+                                                    ctypes.byref(out))
+    if st != DQ_OK:
+        raise DQError(st)
+    return int(out.value)
+
+
+def dq_paged_attention(q, q_dtype, q_stride, k_cache, v_cache, cache_dtype, k_scale, v_scale, page_table, lengths,
+                       batch, q_heads, kv_heads, head_dim, num_pages, page_size, max_pages, window, sinks,
+                       softmax_scale, out, lse, workspace, workspace_bytes, stream) -> int:
+    """Raw call: pointers are ints (0/None for NULL). Returns the dq_status."""
+    return _lib.dq_paged_attention(q, q_dtype, q_stride, k_cache, v_cache, cache_dtype, k_scale, v_scale, page_table,
+                                   lengths, batch, q_heads, kv_heads, head_dim, num_pages, page_size, max_pages,
+                                   window, sinks, softmax_scale, out, lse, workspace, workspace_bytes, stream)
+
+
 # ---------------------------------------------------------------- tensor-level helpers
 
 def _torch():
@@ -148,12 +212,16 @@ def _torch():
     return torch
 
 
+_FLOAT_CODES: dict = {}
+
+
 def _dtype_code(t) -> int:
-    torch = _torch()
-    m = {torch.float32: DQ_F32, torch.float16: DQ_F16, torch.bfloat16: DQ_BF16}
-    if t.dtype not in m:
+    if not _FLOAT_CODES:
+        torch = _torch()
+        _FLOAT_CODES.update({torch.float32: DQ_F32, torch.float16: DQ_F16, torch.bfloat16: DQ_BF16})
+    if t.dtype not in _FLOAT_CODES:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return _FLOAT_CODES[t.dtype]
 
 
 def _dev_ptr(t, name: str) -> int | None:
@@ -338,3 +406,283 @@ def w8a8_gemm(a, b, a_scale, b_scale, out_dtype=None, out=None, accumulate: bool
     if check and st != DQ_OK:
         raise DQError(st)
     return out
+
+
+# The helpers below check every tensor's shape, type and device on the host:
+# the kernels index by the sizes they are given. The launch goes to the
+# tensors' device whatever the current one is, on that device's current stream
+# or on `stream` (a cudaStream_t); what a helper allocates is allocated for that
+# stream, so the allocator does not hand it on while the kernel still uses it.
+
+_ACTIVATIONS = {None: DQ_ACT_NONE, "none": DQ_ACT_NONE, "relu": DQ_ACT_RELU, "gelu": DQ_ACT_GELU,
+                "gelu_tanh": DQ_ACT_GELU_TANH, "silu": DQ_ACT_SILU}
+
+
+def _on(device, stream):
+    """The context to allocate and launch in: the device current, and `stream` when one is given."""
+    torch = _torch()
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                                 else torch.cuda.default_stream(device))
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _expect(name: str, t, shape, dtype) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _cuda_first(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _head_rows(name: str, t, dtype=None):
+    """[tokens, heads, head_dim] with dense heads -> (pointer, elements between tokens)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    tokens, heads, dim = t.shape
+    row, head, one = t.stride()
+    if t.numel() == 0:
+        return t.data_ptr(), heads * dim
+    if (dim > 1 and one != 1) or (heads > 1 and head != dim) or (tokens > 1 and row < heads * dim):
+        raise ValueError(f"{name}: the heads of a token must lie densely one after the other")
+    return t.data_ptr(), (row if tokens > 1 else heads * dim)
+
+
+def w8a8_linear(a, b, a_scale, b_scale, bias=None, activation=None, residual=None, out_dtype=None, out=None,
+                stream=None, check: bool = True):
+    """out = act(float(a @ b.T) * (a_scale[:, None] * b_scale[None, :]) + bias) + residual.
+
+    ``a``: CUDA int8 [M, K]; ``b``: CUDA int8 [N, K]; scales float32 [M], [N];
+    ``bias``: float [N] or None; ``activation``: None / "none", "relu",
+    "gelu", "gelu_tanh" or "silu"; ``residual``: [M, N] of the output's dtype
+    or None, and may be ``out`` itself. Returns the [M, N] output
+    (``out_dtype`` default: the residual's dtype, else float32).
+    """
+    torch = _torch()
+    if a.dim() != 2 or b.dim() != 2 or a.dtype != torch.int8 or b.dtype != torch.int8:
+        raise TypeError("a and b must be 2-D int8 tensors")
+    (m, k), n = a.shape, b.shape[0]
+    if b.shape[1] != k:
+        raise ValueError(f"b must be [N, K] with the K of a ({k}), got {tuple(b.shape)}")
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"unknown activation {activation!r}")
+    _expect("a_scale", a_scale, (m,), torch.float32)
+    _expect("b_scale", b_scale, (n,), torch.float32)
+    if bias is not None:
+        _expect("bias", bias, (n,), bias.dtype)
+    if out is not None:
+        out_dtype = out.dtype if out_dtype is None else out_dtype
+    elif out_dtype is None:
+        out_dtype = torch.float32 if residual is None else residual.dtype
+    if residual is not None:
+        _expect("residual", residual, (m, n), out_dtype)
+    if out is not None:
+        _expect("out", out, (m, n), out_dtype)
+    device = _cuda_first(a, "a")
+    _same_device(device, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, residual=residual, out=out)
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty((m, n), dtype=out_dtype, device=device)
+        if stream is None:
+            stream = torch.cuda.current_stream(device).cuda_stream
+        st = dq_w8a8_linear(_dev_ptr(a, "a"), _dev_ptr(b, "b"), m, n, k, _dev_ptr(a_scale, "a_scale"),
+                            _dev_ptr(b_scale, "b_scale"), _dev_ptr(bias, "bias"),
+                            DQ_F32 if bias is None else _dtype_code(bias), _ACTIVATIONS[activation],
+                            _dev_ptr(residual, "residual"), _dev_ptr(out, "out"), _dtype_code(out), stream)
+    if check and st != DQ_OK:
+        raise DQError(st)
+    return out
+
+
+def _norm_rope_inputs(q, k, positions, inv_freq, q_weight, k_weight):
+    """Shared checks: (device, tokens, q_heads, kv_heads, head_dim, rope_dim, weight dtype code)."""
+    torch = _torch()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [tokens, heads, head_dim]")
+    tokens, q_heads, dim = q.shape
+    kv_heads = k.shape[1]
+    _expect("k", k, (tokens, kv_heads, dim), q.dtype)
+    _expect("positions", positions, (tokens,), torch.int32)
+    rope_dim = 0
+    if inv_freq is not None:
+        rope_dim = 2 * inv_freq.numel()
+        _expect("inv_freq", inv_freq, (rope_dim // 2,), torch.float32)
+    weight = q_weight if q_weight is not None else k_weight
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _expect(name, w, (dim,), weight.dtype)
+    device = _cuda_first(q, "q")
+    _same_device(device, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
+    return device, tokens, q_heads, kv_heads, dim, rope_dim, DQ_F32 if weight is None else _dtype_code(weight)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, epsilon: float = 1e-6,
+                 interleaved: bool = False, out=None, stream=None, check: bool = True):
+    """RMS norm of every query and key head with the position rotation, in one pass.
+
+    ``q``, ``k``: CUDA float16 / bfloat16 [tokens, heads, head_dim], the heads
+    of a token dense (slices of a fused projection work as they are);
+    ``positions``: int32 [tokens]; ``inv_freq``: float32 [rope_dim / 2] or
+    None (no rotation); weights: [head_dim] or None. ``out`` may pass
+    ``(q_out, k_out)``, also ``(q, k)`` themselves. Returns ``(q_out, k_out)``.
+    """
+    torch = _torch()
+    device, tokens, q_heads, kv_heads, dim, rope_dim, wdt = _norm_rope_inputs(q, k, positions, inv_freq, q_weight,
+                                                                              k_weight)
+    with _on(device, stream):
+        if out is None:
+            q_out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=device)
+            k_out = torch.empty((tokens, kv_heads, dim), dtype=q.dtype, device=device)
+        else:
+            q_out, k_out = out
+            _expect("q_out", q_out, q.shape, q.dtype)
+            _expect("k_out", k_out, k.shape, q.dtype)
+            _same_device(device, q_out=q_out, k_out=k_out)
+        if stream is None:
+            stream = torch.cuda.current_stream(device).cuda_stream
+        st = dq_qk_norm_rope(*_head_rows("q", q), *_head_rows("k", k), _dtype_code(q), tokens, q_heads, kv_heads, dim,
+                             _dev_ptr(q_weight, "q_weight"), _dev_ptr(k_weight, "k_weight"), wdt, float(epsilon),
+                             _dev_ptr(positions, "positions"), _dev_ptr(inv_freq, "inv_freq"), rope_dim,
+                             1 if interleaved else 0, *_head_rows("q_out", q_out), *_head_rows("k_out", k_out), stream)
+    if check and st != DQ_OK:
+        raise DQError(st)
+    return q_out, k_out
+
+
+def _cache_tensors(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, device):
+    """Shared checks of a paged cache: (num_pages, page_size, cache dtype code)."""
+    torch = _torch()
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, kv_heads, page_size, head_dim]")
+    pages, page_size = k_cache.shape[0], k_cache.shape[2]
+    codes = k_cache.dtype == torch.int8
+    if not codes and k_cache.dtype != dtype:
+        raise TypeError(f"k_cache must be {dtype} or torch.int8, got {k_cache.dtype}")
+    _expect("k_cache", k_cache, (pages, kv_heads, page_size, dim), k_cache.dtype)
+    _expect("v_cache", v_cache, k_cache.shape, k_cache.dtype)
+    _same_device(device, k_cache=k_cache, v_cache=v_cache)
+    if codes:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an int8 cache needs k_scale and v_scale")
+        _expect("k_scale", k_scale, (pages, kv_heads, page_size), torch.float32)
+        _expect("v_scale", v_scale, (pages, kv_heads, page_size), torch.float32)
+        _same_device(device, k_scale=k_scale, v_scale=v_scale)
+        return pages, page_size, DQ_INT8
+    return pages, page_size, _dtype_code(k_cache)
+
+
+def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_scale=None, v_scale=None,
+                       q_weight=None, k_weight=None, epsilon: float = 1e-6, interleaved: bool = False, out=None,
+                       stream=None, check: bool = True):
+    """``qk_norm_rope`` with the keys, and the values as they are, written into a paged cache.
+
+    ``k_cache``, ``v_cache``: [num_pages, kv_heads, page_size, head_dim] of
+    q's dtype, or int8 with float32 ``k_scale``, ``v_scale`` [num_pages,
+    kv_heads, page_size]; ``slots``: int64 [tokens], page * page_size + row,
+    negative for a token that is not stored. ``out`` may pass ``q_out``, also
+    ``q`` itself. Returns ``q_out``; the caches are updated in place.
+    """
+    torch = _torch()
+    device, tokens, q_heads, kv_heads, dim, rope_dim, wdt = _norm_rope_inputs(q, k, positions, inv_freq, q_weight,
+                                                                              k_weight)
+    _expect("v", v, (tokens, kv_heads, dim), q.dtype)
+    _expect("slots", slots, (tokens,), torch.int64)
+    _same_device(device, v=v, slots=slots)
+    pages, page_size, cdt = _cache_tensors(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, q.dtype, device)
+    codes = cdt == DQ_INT8
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=device)
+        else:
+            _expect("out", out, q.shape, q.dtype)
+            _same_device(device, out=out)
+        if stream is None:
+            stream = torch.cuda.current_stream(device).cuda_stream
+        st = dq_qk_norm_rope_cache(*_head_rows("q", q), *_head_rows("k", k), *_head_rows("v", v), _dtype_code(q),
+                                   tokens, q_heads, kv_heads, dim, _dev_ptr(q_weight, "q_weight"),
+                                   _dev_ptr(k_weight, "k_weight"), wdt, float(epsilon),
+                                   _dev_ptr(positions, "positions"), _dev_ptr(inv_freq, "inv_freq"), rope_dim,
+                                   1 if interleaved else 0, *_head_rows("out", out), _dev_ptr(k_cache, "k_cache"),
+                                   _dev_ptr(v_cache, "v_cache"), cdt, _dev_ptr(k_scale, "k_scale") if codes else None,
+                                   _dev_ptr(v_scale, "v_scale") if codes else None, _dev_ptr(slots, "slots"), pages,
+                                   page_size, stream)
+    if check and st != DQ_OK:
+        raise DQError(st)
+    return out
+
+
+def paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale=None, v_scale=None, softmax_scale=None,
+                    window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None,
+                    check: bool = True):
+    """Attention of one new token per sequence over a paged key-value cache.
+
+    ``q``: CUDA float16 / bfloat16 [batch, q_heads, head_dim], dense heads;
+    the cache as ``qk_norm_rope_cache`` writes it; ``page_table``: int32
+    [batch, max_pages]; ``lengths``: int32 [batch], the new token included;
+    ``softmax_scale``: default head_dim ** -0.5; ``window``: 0, or the number
+    of last tokens that are visible beside the first ``sinks``; ``lse``: an
+    optional float32 [batch, q_heads] output; ``workspace``: an optional
+    preallocated CUDA tensor of at least
+    ``dq_paged_attention_get_workspace_size`` bytes. Returns [batch, q_heads,
+    head_dim] of q's dtype.
+    """
+    torch = _torch()
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q must be [batch, q_heads, head_dim] and k_cache [num_pages, kv_heads, page_size, head_dim]")
+    batch, q_heads, dim = q.shape
+    kv_heads = k_cache.shape[1]
+    device = _cuda_first(q, "q")
+    pages, page_size, cdt = _cache_tensors(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, q.dtype, device)
+    codes = cdt == DQ_INT8
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch, max_pages]")
+    max_pages = page_table.shape[1]
+    _expect("page_table", page_table, (batch, max_pages), torch.int32)
+    _expect("lengths", lengths, (batch,), torch.int32)
+    if lse is not None:
+        _expect("lse", lse, (batch, q_heads), torch.float32)
+    _same_device(device, page_table=page_table, lengths=lengths, lse=lse, workspace=workspace)
+    ws_bytes = dq_paged_attention_get_workspace_size(batch, q_heads, kv_heads, dim, cdt)
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty((batch, q_heads, dim), dtype=q.dtype, device=device)
+        else:
+            _expect("out", out, q.shape, q.dtype)
+            _same_device(device, out=out)
+        if workspace is None and ws_bytes:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+        if workspace is not None:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        if stream is None:
+            stream = torch.cuda.current_stream(device).cuda_stream
+        st = dq_paged_attention(*_q_rows(q), _dev_ptr(k_cache, "k_cache"),
+                                _dev_ptr(v_cache, "v_cache"), cdt, _dev_ptr(k_scale, "k_scale") if codes else None,
+                                _dev_ptr(v_scale, "v_scale") if codes else None, _dev_ptr(page_table, "page_table"),
+                                _dev_ptr(lengths, "lengths"), batch, q_heads, kv_heads, dim, pages, page_size,
+                                max_pages, int(window), int(sinks),
+                                float(dim ** -0.5 if softmax_scale is None else softmax_scale), _dev_ptr(out, "out"),
+                                _dev_ptr(lse, "lse"), _dev_ptr(workspace, "workspace"), ws_bytes, stream)
+    if check and st != DQ_OK:
+        raise DQError(st)
+    return out
+
+
+def _q_rows(q):
+    """(pointer, dtype code, elements between sequences) of paged_attention's q."""
+    ptr, stride = _head_rows("q", q)
+    return ptr, _dtype_code(q), stride
