@@ -14,51 +14,12 @@
 #include "dq.h"
 #include "dq_device.cuh"
 #include "dq_launch.cuh"
+#include "paged_attention_args.cuh"
+#include "paged_attention_mma.cuh"
 
 namespace dq {
 
-struct PagedArgs {
-  const void* q;
-  int64_t q_stride;
-  const void* k_cache;
-  const void* v_cache;
-  const float* k_scale;
-  const float* v_scale;
-  const int32_t* page_table;
-  const int32_t* lengths;
-  int64_t batch;
-  int q_heads, kv_heads, head_dim, group;  // group: query heads per key head
-  int64_t num_pages;
-  int page_size;
-  int64_t max_pages;
-  int64_t window, sinks;
-  float softmax_scale;
-  void* out;
-  float* lse;
-};
-
-// The visible tokens of one sequence: `count` of them, number i being token
-// i (i < first) or i + skip. A length that the page table cannot hold is one
-// visible token past the table, which makes the rows NaN.
-struct Visible {
-  int64_t count, first, skip;
-};
-
-__device__ __forceinline__ Visible visible_tokens(const PagedArgs& a, int64_t b) {
-  const int64_t len = a.lengths[b];
-  const int64_t room = a.max_pages * a.page_size;
-  if (len <= 0) return {0, 0, 0};
-  if (len > room) return {1, 0, room};
-  if (a.window == 0 || len <= a.window) return {len, len, 0};
-  const int64_t start = len - a.window;
-  const int64_t first = a.sinks < start ? a.sinks : start;
-  return {first + a.window, first, start - first};
-}
-
 constexpr int kPagedGenericWarps = 4;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
 __device__ __forceinline__ float load_row(const __half* p, int64_t i) { return __half2float(p[i]); }
 __device__ __forceinline__ float load_row(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
 __device__ __forceinline__ float load_row(const int8_t* p, int64_t i) { return static_cast<float>(p[i]); }
@@ -160,6 +121,72 @@ dq_status launch_generic(const dq::PagedArgs& a, cudaStream_t stream) {
                                       stream);
 }
 
+// ---- tensor-core path
+
+// Query heads of one item: two sets of 8 where a key head serves more than 8
+// and the accumulators fit (16 heads of 256 channels do not).
+constexpr int head_tiles(int group, int dim) { return group > 8 && dim <= 128 ? 2 : 1; }
+
+// CTAs that share the tiles at most: what fits the device at once, four to an SM.
+int64_t most_ctas() { return static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * 4; }
+
+bool mma_dim(int dim) { return dim == 64 || dim == 128 || dim == 256; }
+
+size_t parts_bytes(int group, int dim) {
+  const int heads = 8 * head_tiles(group, dim);
+  return static_cast<size_t>(most_ctas()) * 2 * (heads * dim + 2 * heads) * sizeof(float);
+}
+
+template <typename T, typename C, int D, int HT>
+dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
+  using Shape = dq::PagedShape<C, D, HT>;
+  void (*fn)(const dq::PagedArgs) = dq::paged_attention_mma_kernel<T, C, D, HT>;
+  const int device = dq_host::current_device();
+  if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
+  a.head_sets = (a.group + Shape::kHeads - 1) / Shape::kHeads;
+  a.items = a.batch * a.kv_heads * a.head_sets;
+  int64_t ctas = static_cast<int64_t>(dq_host::sm_count(device)) *
+                 dq_host::blocks_per_sm(reinterpret_cast<const void*>(fn), dq::kPagedThreads, Shape::kSmem, device);
+  if (ctas > most_ctas()) ctas = most_ctas();
+  a.whole = 0;
+  dq_status st = dq_host::launch_programmatic(fn, a, static_cast<int>(ctas), dq::kPagedThreads, Shape::kSmem, stream);
+  if (st != DQ_OK) return st;
+  const int by_item = a.items < ctas ? 1 : 0;
+  const int heads = a.group < Shape::kHeads ? a.group : Shape::kHeads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(by_item ? a.items : ctas - 1), by_item ? heads : 1);
+  cfg.blockDim = dim3(dq::kPagedThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void (*join)(const dq::PagedArgs, const int, const int) = dq::paged_attention_join_kernel<T, C, D, HT>;
+  if (cudaLaunchKernelEx(&cfg, join, a, static_cast<int>(ctas), by_item) != cudaSuccess) {
+    cudaGetLastError();
+    return DQ_ERR_CUDA;
+  }
+  return dq_host::launch_status();
+}
+
+template <typename T, typename C>
+dq_status dispatch_mma(const dq::PagedArgs& a, cudaStream_t stream) {
+  const int ht = head_tiles(a.group, a.head_dim);
+  if (a.head_dim == 64) return ht == 2 ? launch_mma<T, C, 64, 2>(a, stream) : launch_mma<T, C, 64, 1>(a, stream);
+  if (a.head_dim == 128) return ht == 2 ? launch_mma<T, C, 128, 2>(a, stream) : launch_mma<T, C, 128, 1>(a, stream);
+  return launch_mma<T, C, 256, 1>(a, stream);
+}
+
+template <typename T, typename C>
+dq_status dispatch(const dq::PagedArgs& a, bool mma, cudaStream_t stream) {
+  if (mma) {
+    const dq_status st = dispatch_mma<T, C>(a, stream);
+    if (st != dq_host::kNotLaunchable) return st;
+  }
+  return launch_generic<T, C>(a, stream);
+}
+
 dq_status check_heads(int64_t batch, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   if (batch < 0 || batch > 65535 * 16 || q_heads < 1 || q_heads > DQ_MAX_HEADS || kv_heads < 1 ||
       kv_heads > DQ_MAX_HEADS || q_heads % kv_heads != 0 || head_dim < 1 || head_dim > DQ_MAX_HEAD_DIM)
@@ -178,7 +205,7 @@ extern "C" dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_
   const dq_status st = check_heads(batch, q_heads, kv_heads, head_dim);
   if (st != DQ_OK) return st;
   if (!is_cache(cache_dtype)) return DQ_ERR_BAD_DTYPE;
-  *workspace_bytes = 0;
+  *workspace_bytes = batch > 0 && mma_dim(head_dim) ? parts_bytes(q_heads / kv_heads, head_dim) : 0;
   return DQ_OK;
 }
 
@@ -235,9 +262,19 @@ extern "C" dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t
   a.softmax_scale = softmax_scale;
   a.out = out;
   a.lse = lse;
+  // token / page_size for tokens below 2^31: shift = ceil(log2 d), mul = 2^32 (2^shift - d) / d + 1
+  uint32_t shift = 0;
+  while ((int64_t(1) << shift) < page_size) ++shift;
+  a.page_shift = shift;
+  a.page_mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - page_size)) / page_size + 1);
+  a.parts = static_cast<float*>(workspace);
+  // 16-byte pieces of cache rows, 8-byte pieces of q and out rows, row numbers below 2^32
+  const bool mma = mma_dim(head_dim) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(q, 8) &&
+                   q_stride % 4 == 0 && aligned(out, 8) &&
+                   num_pages <= int64_t(0xFFFFFFF0u) / page_size / kv_heads;
   if (q_dtype == DQ_F16) {
-    return codes ? launch_generic<__half, int8_t>(a, stream) : launch_generic<__half, __half>(a, stream);
+    return codes ? dispatch<__half, int8_t>(a, mma, stream) : dispatch<__half, __half>(a, mma, stream);
   }
-  return codes ? launch_generic<__nv_bfloat16, int8_t>(a, stream)
-               : launch_generic<__nv_bfloat16, __nv_bfloat16>(a, stream);
+  return codes ? dispatch<__nv_bfloat16, int8_t>(a, mma, stream)
+               : dispatch<__nv_bfloat16, __nv_bfloat16>(a, mma, stream);
 }

@@ -1,0 +1,682 @@
+// Paged decode attention on the tensor cores: one pass over the visible rows
+// of the cache, straight from global memory into the matrix operands'
+// registers.
+//
+// One product serves up to 8 * HT query heads of a key head at once, the
+// tokens along the matrix rows so that few heads waste nothing:
+//   S^T[token, head] = K[token, :] . Q[head, :]       m16n8k16, K as the A operand
+//   O^T[dim, head]  += V^T[dim, token] . P[token, head]  V^T as the A operand
+// The order of the contracted index is free as long as both operands share
+// it, and so is the order of the rows of O^T. A lane (g = lane / 4, t = lane % 4)
+// therefore loads 16-byte pieces of the K rows g and g + 8 (pieces t of every 4)
+// and of the V rows of its tokens (pieces g of every 8), each used whole: no
+// shared memory and no barrier stand between the cache and the products.
+// movmatrix turns P from the accumulator's layout into the B operand's.
+//
+// Codes become f16 by byte permutes: 0x64xx is 1024 + xx, so (code ^ 0x80) in the
+// low byte gives 1152 + code, and one f16 subtraction leaves the code, exact.
+// Query rows beside codes are scaled by a power of two per head into f16's
+// range; value scales are folded into the weights relative to the power of two
+// of the largest one so far, so weights keep 11 bits whatever the scales' size.
+//
+// The running maximum moves only when a score exceeds it by 8 (in log2): weights
+// then stay below 2^(8 + kLift) and the rescaling of O is rare. kLift raises
+// the weights in f16 so that those down to 2^-30 of the largest count.
+//
+// Work: all (sequence, key head, head set) items' tiles of TT tokens, laid end
+// to end, are cut into equal ranges, one per CTA, whatever the lengths; a CTA's
+// warps take its tiles in turn. Items inside one range are finished by their
+// CTA. Of an item that ranges cut, each CTA leaves (max, sum, O) in the
+// workspace, and a second kernel joins them.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "dq_device.cuh"
+#include "paged_attention_args.cuh"
+
+namespace dq {
+
+constexpr int kPagedWarps = 4;
+constexpr int kPagedThreads = kPagedWarps * 32;
+constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the running maximum
+constexpr float kLift = 6.0f;   // log2 of the weight at the running maximum
+constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;
+
+template <typename C, int D, int HT>
+struct PagedShape {
+  static constexpr bool kCodes = sizeof(C) == 1;
+  // 4 KB of K and of V in flight per warp, a multiple of 16 tokens, at most one token per lane
+  static constexpr int kFit = 4096 / (D * int(sizeof(C)));
+  static constexpr int kTokens = kFit >= 32 ? 32 : 16;
+  static constexpr int kHeads = 8 * HT;
+  // one CTA's parts: O [kHeads][D], then (max, sum) [kHeads]
+  static constexpr int kPartFloats = kHeads * D + 2 * kHeads;
+  static constexpr size_t kSmem = size_t(kPagedWarps) * (kHeads * D + 2 * kHeads) * 4;
+};
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
+
+// Transpose of an 8x8 matrix of 16-bit values held two to a lane.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (kBf16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  } else {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two codes, biased by 128 in bytes `sel` of w, as exact f16 values.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
+  const uint32_t h = prmt(w, 0x64646464u, sel);
+  const uint32_t bias = 0x64806480u;  // 1152
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_piece(uint32_t (&r)[BYTES / 4], const void* p) {
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+  }
+}
+
+// ---------------------------------------------------------------- the schedule
+
+// Tiles of one sequence's item; a sequence without tokens still has one, whose
+// CTA writes its zeros.
+template <int TT>
+__device__ __forceinline__ int64_t item_tiles(const PagedArgs& a, int64_t b) {
+  const int64_t n = (visible_tokens(a, b).count + TT - 1) / TT;
+  return n < 1 ? 1 : n;
+}
+
+__device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// All tiles of the call (every lane of the warp gets the sum).
+template <int TT>
+__device__ int64_t total_tiles(const PagedArgs& a) {
+  int64_t sum = 0;
+  const int lane = threadIdx.x & 31;
+  for (int64_t b = lane; b < a.batch; b += 32) sum += item_tiles<TT>(a, b);
+  return warp_sum_i64(sum) * a.kv_heads * a.head_sets;
+}
+
+// The sequence that tile `x` belongs to, and the number of its first tile.
+template <int TT>
+__device__ void find_sequence(const PagedArgs& a, int64_t x, int64_t& seq, int64_t& base) {
+  const int lane = threadIdx.x & 31;
+  const int64_t per = static_cast<int64_t>(a.kv_heads) * a.head_sets;
+  int64_t before = 0;
+  for (int64_t b0 = 0;; b0 += 32) {
+    const int64_t b = b0 + lane;
+    int64_t end = b < a.batch ? item_tiles<TT>(a, b) * per : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += up;
+    }
+    end += before;
+    const uint32_t hit = __ballot_sync(0xffffffffu, b < a.batch && end > x);
+    if (hit != 0u || b0 + 32 >= a.batch) {
+      const int first = hit != 0u ? __ffs(hit) - 1 : 0;
+      const int64_t prev = __shfl_up_sync(0xffffffffu, end, 1);
+      seq = b0 + first;
+      base = first == 0 ? before : __shfl_sync(0xffffffffu, prev, first);
+      return;
+    }
+    before = __shfl_sync(0xffffffffu, end, 31);
+  }
+}
+
+// Tiles per CTA: equal shares, and at least one for each warp.
+__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int64_t ctas) {
+  const int64_t per = (total + ctas - 1) / ctas;
+  return per < kPagedWarps ? kPagedWarps : per;
+}
+
+// ---------------------------------------------------------------- main kernel
+
+template <typename T, typename C, int D, int HT>
+__global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(const PagedArgs a) {
+  using Shape = PagedShape<C, D, HT>;
+  constexpr bool kCodes = Shape::kCodes;
+  constexpr bool kBf16 = !kCodes && sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
+  constexpr int TT = Shape::kTokens, MT = TT / 16, kHeads = Shape::kHeads;
+  constexpr int kElem = sizeof(C);
+  constexpr int kPiece = 16 / kElem;         // elements of a 16-byte piece
+  constexpr int KP = D / (4 * kPiece);       // K pieces per lane and row
+  constexpr int kVBytes = D * kElem / 8 >= 16 ? 16 : D * kElem / 8;
+  constexpr int kVPiece = kVBytes / kElem;   // elements of a V piece
+  constexpr int VP = D / (8 * kVPiece);      // V pieces per lane and row
+  constexpr int KS = D / 16;                 // k-steps of S, and row tiles of O^T
+  extern __shared__ float smem[];            // [warps][kHeads][D], [warps][kHeads][2]
+  float* s_o = smem;
+  float* s_stat = smem + kPagedWarps * kHeads * D;
+
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+
+  int64_t seq, base, tile, tile_end;
+  const int64_t items_per_seq = static_cast<int64_t>(a.kv_heads) * a.head_sets;
+  if (a.whole) {
+    seq = blockIdx.x / items_per_seq;
+    const int64_t n = item_tiles<TT>(a, seq);
+    base = 0;
+    tile = (blockIdx.x - seq * items_per_seq) * n;
+    tile_end = tile + n;
+  } else {
+    const int64_t total = total_tiles<TT>(a);
+    const int64_t per = tiles_per_cta(total, gridDim.x);
+    tile = per * blockIdx.x;
+    tile_end = tile + per < total ? tile + per : total;
+    if (tile >= total) return;
+    find_sequence<TT>(a, tile, seq, base);
+  }
+  const int64_t range_begin = tile;
+
+  while (tile < tile_end) {
+    const Visible vis = visible_tokens(a, seq);
+    const int64_t n = vis.count < 1 ? 1 : (vis.count + TT - 1) / TT;
+    const int64_t item = (tile - base) / n;
+    const int64_t item_begin = base + item * n;
+    const int t0 = static_cast<int>(tile - item_begin);
+    const int t1 = static_cast<int>((item_begin + n < tile_end ? item_begin + n : tile_end) - item_begin);
+    const int kvh = static_cast<int>(item / a.head_sets);
+    const int set = static_cast<int>(item - static_cast<int64_t>(kvh) * a.head_sets);
+    const int head0 = kvh * a.group + set * kHeads;                        // first query head
+    const int heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
+    const uint32_t count = static_cast<uint32_t>(vis.count), first = static_cast<uint32_t>(vis.first);
+    const int32_t* table = a.page_table + seq * a.max_pages;
+
+    // Q as B operands: head g, four channels per k-step
+    uint32_t qf[HT][KS][2];
+    float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+      const bool on = 8 * ht + g < heads;
+      const T* q = static_cast<const T*>(a.q) + seq * a.q_stride + static_cast<int64_t>(head0 + 8 * ht + g) * D;
+      float mul = a.softmax_scale * kLog2e;
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        const int c = (s / (kPiece / 4)) * 4 * kPiece + kPiece * t + 4 * (s % (kPiece / 4));
+        uint2 w = make_uint2(0u, 0u);
+        if (on) w = *reinterpret_cast<const uint2*>(q + c);
+        qf[ht][s][0] = w.x;
+        qf[ht][s][1] = w.y;
+      }
+      if constexpr (kCodes && __is_same(T, __nv_bfloat16)) {
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ht][s][i] << 16)),
+                                   fabsf(__uint_as_float(qf[ht][s][i] & 0xFFFF0000u))));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // scaled so that the largest channel lies in [2^14, 2^15): exact down to 2^-28 of it
+        const int e = top > 0.0f && isfinite(top) ? 14 - ilogbf(top) : 0;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            qf[ht][s][i] = pack_f16(scalbnf(__uint_as_float(qf[ht][s][i] << 16), e),
+                                    scalbnf(__uint_as_float(qf[ht][s][i] & 0xFFFF0000u), e));
+          }
+        }
+        mul = scalbnf(mul, -e);
+      }
+      q_mul[ht][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
+      q_mul[ht][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
+    }
+
+    float o[HT][KS][4], m[HT][2], l[HT][2];
+    float v_top = 0.0f, v_mul = 1.0f;  // largest value scale so far, and the power of two that takes it below 2
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+      m[ht][0] = m[ht][1] = -INFINITY;
+      l[ht][0] = l[ht][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.0f;
+    }
+
+    // lane r finds the cache row of token r of a tile, in two steps so that the
+    // table's latency is off the path: the page, one tile ahead of the row
+    const auto find_page = [&](int tl, uint32_t& in_page) -> int32_t {
+      const uint32_t i = static_cast<uint32_t>(tl) * TT + lane;
+      if (tl >= t1 || lane >= TT || i >= count) return -2;
+      const uint32_t j = i < first ? i : i + static_cast<uint32_t>(vis.skip);
+      const uint32_t p = (__umulhi(j, a.page_mul) + j) >> a.page_shift;
+      in_page = j - p * static_cast<uint32_t>(a.page_size);
+      return p < a.max_pages ? max(__ldg(table + p), -1) : -1;
+    };
+    const auto row_of = [&](int32_t page, uint32_t in_page) -> uint32_t {
+      if (page == -2) return kRowHidden;
+      if (page < 0 || page >= a.num_pages) return kRowBad;
+      return (static_cast<uint32_t>(page) * static_cast<uint32_t>(a.kv_heads) + static_cast<uint32_t>(kvh)) *
+                 static_cast<uint32_t>(a.page_size) + in_page;
+    };
+
+    uint32_t kr[MT][2][KP][4];                   // K pieces of rows g and g + 8
+    uint32_t vr[MT][4][VP][kVBytes / 4];         // V pieces of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+    uint32_t krow[MT][2];                        // cache rows of tokens g and g + 8
+    float ks[MT][2], vs[MT][2];
+    const auto load_k = [&](uint32_t row) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * mt + 8 * h + g);
+          krow[mt][h] = r;
+          const bool on = r < kRowBad;
+          const C* p = static_cast<const C*>(a.k_cache) + static_cast<uint64_t>(r) * D + kPiece * t;
+#pragma unroll
+          for (int i = 0; i < KP; ++i) {
+            if (on) {
+              load_piece<16>(kr[mt][h][i], p + 4 * kPiece * i);
+            } else {
+              kr[mt][h][i][0] = kr[mt][h][i][1] = kr[mt][h][i][2] = kr[mt][h][i][3] = 0u;
+            }
+          }
+          if constexpr (kCodes) {
+            ks[mt][h] = on ? __ldg(a.k_scale + r) : 0.0f;
+            vs[mt][h] = on ? __ldg(a.v_scale + r) : 0.0f;
+          }
+        }
+      }
+    };
+    const auto load_v = [&](uint32_t row) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1));
+          const C* p = static_cast<const C*>(a.v_cache) + static_cast<uint64_t>(r) * D + kVPiece * g;
+#pragma unroll
+          for (int i = 0; i < VP; ++i) {
+            if (r < kRowBad) {
+              load_piece<kVBytes>(vr[mt][k][i], p + 8 * kVPiece * i);
+            } else {
+#pragma unroll
+              for (int w = 0; w < kVBytes / 4; ++w) vr[mt][k][i][w] = 0u;
+            }
+          }
+        }
+      }
+    };
+
+    int tl = t0 + warp;
+    uint32_t in_page = 0u, in_page_next = 0u;
+    int32_t page = find_page(tl, in_page);
+    uint32_t row = row_of(page, in_page);
+    int32_t page_next = find_page(tl + kPagedWarps, in_page_next);
+    if (tl < t1) {
+      load_k(row);
+      load_v(row);
+    }
+    for (; tl < t1; tl += kPagedWarps) {
+      // ---- S^T = K Q^T
+      float s[HT][MT][4];
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) s[ht][mt][0] = s[ht][mt][1] = s[ht][mt][2] = s[ht][mt][3] = 0.0f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+          if constexpr (kCodes) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t w0 = kr[mt][0][i][u] ^ 0x80808080u, w1 = kr[mt][1][i][u] ^ 0x80808080u;
+              const uint32_t a0 = codes_f16(w0, 0x4140u), a2 = codes_f16(w0, 0x4342u);
+              const uint32_t a1 = codes_f16(w1, 0x4140u), a3 = codes_f16(w1, 0x4342u);
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+                mma16816<false>(s[ht][mt], a0, a1, a2, a3, qf[ht][4 * i + u][0], qf[ht][4 * i + u][1]);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht)
+                mma16816<kBf16>(s[ht][mt], kr[mt][0][i][2 * u], kr[mt][1][i][2 * u], kr[mt][0][i][2 * u + 1],
+                                kr[mt][1][i][2 * u + 1], qf[ht][2 * i + u][0], qf[ht][2 * i + u][1]);
+            }
+          }
+        }
+      }
+      // ---- scores in log2, hidden tokens out
+      float vw[MT][2];
+      bool hidden[MT][2];
+      bool move = false;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          hidden[mt][h] = krow[mt][h] == kRowHidden;
+          const bool bad = krow[mt][h] == kRowBad;
+          vw[mt][h] = kCodes ? vs[mt][h] : 1.0f;
+          if (kCodes) move |= vs[mt][h] > v_top;
+#pragma unroll
+          for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float& x = s[ht][mt][2 * h + c];
+              x *= kCodes ? ks[mt][h] * q_mul[ht][c] : q_mul[ht][c];
+              if (hidden[mt][h]) x = -INFINITY;
+              if (bad) x = NAN;
+              move |= x > m[ht][c] + kSlack;
+            }
+          }
+        }
+      }
+      // ---- the next tile's K, its table entries already here
+      row = row_of(page_next, in_page_next);
+      page_next = find_page(tl + 2 * kPagedWarps, in_page_next);
+      const bool more = tl + kPagedWarps < t1;
+      if (more) load_k(row);
+      // ---- the running maximum and the largest value scale, when they have to move
+      if (__any_sync(0xffffffffu, move)) {
+        float v_keep = 1.0f;
+        if constexpr (kCodes) {
+          float top = v_top;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(vw[mt][0], vw[mt][1]));
+#pragma unroll
+          for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+          if (top > v_top) {
+            const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e) takes top into [1, 2)
+            const float next = __uint_as_float((254u - (e < 1u ? 1u : (e > 253u ? 253u : e))) << 23);
+            v_keep = v_top > 0.0f ? next / v_mul : 0.0f;  // nothing but zeros so far: O is 0
+            v_top = top;
+            v_mul = next;
+          }
+        }
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(s[ht][mt][c], s[ht][mt][2 + c]));
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            float keep = 1.0f;
+            if (top > m[ht][c]) {
+              keep = exp2f(m[ht][c] - top);
+              m[ht][c] = top;
+              l[ht][c] *= keep;
+            }
+            keep *= v_keep;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              o[ht][i][c] *= keep;
+              o[ht][i][2 + c] *= keep;
+            }
+          }
+        }
+      }
+      // ---- weights, as the B operand
+      uint32_t p[HT][MT][2], p_lo[HT][MT][2];
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+        const float z0 = (m[ht][0] == -INFINITY ? 0.0f : m[ht][0]) - kLift;
+        const float z1 = (m[ht][1] == -INFINITY ? 0.0f : m[ht][1]) - kLift;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float w0 = exp2f(s[ht][mt][2 * h] - z0), w1 = exp2f(s[ht][mt][2 * h + 1] - z1);
+            l[ht][0] += w0;
+            l[ht][1] += w1;
+            if constexpr (kCodes) {
+              const float f = vw[mt][h] * v_mul;
+              w0 *= f;
+              w1 *= f;
+            }
+            if constexpr (kBf16) {
+              const uint32_t hi = pack_bf16(w0, w1);
+              p[ht][mt][h] = movmatrix(hi);
+              // what bf16 cuts off, kept in a second operand: 16 bits of weight
+              p_lo[ht][mt][h] = movmatrix(pack_bf16(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xFFFF0000u)));
+            } else {
+              p[ht][mt][h] = movmatrix(pack_f16(w0, w1));
+            }
+          }
+        }
+      }
+      // ---- O^T += V^T P
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+#pragma unroll
+          for (int w = 0; w < kVBytes / 4; ++w) {
+            const uint32_t va = vr[mt][0][i][w], vb = vr[mt][1][i][w], vc = vr[mt][2][i][w], vd = vr[mt][3][i][w];
+            if constexpr (kCodes) {  // four channels of two tokens pairs: two row tiles
+              const int tile0 = (i * (kVBytes / 4) + w) * 2;
+              const uint32_t ab01 = prmt(va, vb, 0x5140u) ^ 0x80808080u, ab23 = prmt(va, vb, 0x7362u) ^ 0x80808080u;
+              const uint32_t cd01 = prmt(vc, vd, 0x5140u) ^ 0x80808080u, cd23 = prmt(vc, vd, 0x7362u) ^ 0x80808080u;
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) {
+                mma16816<false>(o[ht][tile0], codes_f16(ab01, 0x4140u), codes_f16(ab01, 0x4342u),
+                                codes_f16(cd01, 0x4140u), codes_f16(cd01, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
+                mma16816<false>(o[ht][tile0 + 1], codes_f16(ab23, 0x4140u), codes_f16(ab23, 0x4342u),
+                                codes_f16(cd23, 0x4140u), codes_f16(cd23, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
+              }
+            } else {  // two channels of two token pairs: one row tile
+              const int tile0 = i * (kVBytes / 4) + w;
+              const uint32_t a0 = prmt(va, vb, 0x5410u), a1 = prmt(va, vb, 0x7632u);
+              const uint32_t a2 = prmt(vc, vd, 0x5410u), a3 = prmt(vc, vd, 0x7632u);
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) {
+                mma16816<kBf16>(o[ht][tile0], a0, a1, a2, a3, p[ht][mt][0], p[ht][mt][1]);
+                if constexpr (kBf16)
+                  mma16816<kBf16>(o[ht][tile0], a0, a1, a2, a3, p_lo[ht][mt][0], p_lo[ht][mt][1]);
+              }
+            }
+          }
+        }
+      }
+      if (more) load_v(row);
+    }
+
+    // ---- join the warps
+    const float v_undo = 1.0f / v_mul;
+    __syncthreads();  // the previous item's readers are done
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[ht][c];
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int h = 8 * ht + 2 * t + c;
+        if (g == 0) {
+          s_stat[(warp * kHeads + h) * 2] = m[ht][c];
+          s_stat[(warp * kHeads + h) * 2 + 1] = sum;
+        }
+        float* dst = s_o + (warp * kHeads + h) * D;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          // row tile i holds the lane's channels 2i and 2i + 1, counted over its V pieces
+          const int e = 2 * i;
+          const int ch = (e / kVPiece) * 8 * kVPiece + kVPiece * g + e % kVPiece;
+          dst[ch] = o[ht][i][c] * v_undo;
+          dst[ch + 1] = o[ht][i][2 + c] * v_undo;
+        }
+      }
+    }
+    __syncthreads();
+    const bool complete = t0 == 0 && item_begin + n <= tile_end;
+    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (item_begin < range_begin ? 0 : 1)) *
+                                static_cast<int64_t>(Shape::kPartFloats);
+    for (int x = threadIdx.x; x < heads * (D / 4); x += kPagedThreads) {
+      const int h = x / (D / 4), c = (x - h * (D / 4)) * 4;
+      float top = -INFINITY, total = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, s_stat[(w * kHeads + h) * 2]);
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kPagedWarps; ++w) {
+        const float mw = s_stat[(w * kHeads + h) * 2];
+        const float f = mw == top ? 1.0f : exp2f(mw - top);
+        total = fmaf(s_stat[(w * kHeads + h) * 2 + 1], f, total);
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * D + c);
+        sum.x = fmaf(v.x, f, sum.x);
+        sum.y = fmaf(v.y, f, sum.y);
+        sum.z = fmaf(v.z, f, sum.z);
+        sum.w = fmaf(v.w, f, sum.w);
+      }
+      if (complete) {
+        const int64_t at = seq * a.q_heads + head0 + h;
+        const float r = vis.count == 0 ? 0.0f : 1.0f / total;
+        T* out = static_cast<T*>(a.out) + at * D + c;
+        uint2 w;
+        if constexpr (__is_same(T, __nv_bfloat16)) {
+          w = make_uint2(pack_bf16(sum.x * r, sum.y * r), pack_bf16(sum.z * r, sum.w * r));
+        } else {
+          w = make_uint2(pack_f16(sum.x * r, sum.y * r), pack_f16(sum.z * r, sum.w * r));
+        }
+        *reinterpret_cast<uint2*>(out) = w;
+        if (a.lse != nullptr && c == 0)
+          a.lse[at] = vis.count == 0 ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(part + h * D + c) = sum;
+        if (c == 0) {
+          part[kHeads * D + 2 * h] = top;
+          part[kHeads * D + 2 * h + 1] = total;
+        }
+      }
+    }
+    tile += t1 - t0;
+    if (tile == base + n * items_per_seq) {  // on to the next sequence
+      base = tile;
+      ++seq;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- joining kernel
+
+// Joins what CTAs have left of an item that their ranges cut. By item where
+// there are fewer items than CTAs, else one CTA per border between ranges (the
+// first border inside an item takes it); the heads spread over grid.y.
+template <typename T, typename C, int D, int HT>
+__global__ void __launch_bounds__(kPagedThreads) paged_attention_join_kernel(const PagedArgs a, const int ctas,
+                                                                             const int by_item) {
+  using Shape = PagedShape<C, D, HT>;
+  constexpr int TT = Shape::kTokens, kHeads = Shape::kHeads;
+  constexpr int kVec = D / 4, kSplit = kPagedThreads / kVec < 1 ? 1 : kPagedThreads / kVec;
+  __shared__ float s_o[kSplit][D];
+  __shared__ float s_m[kSplit], s_l[kSplit];
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int64_t items_per_seq = static_cast<int64_t>(a.kv_heads) * a.head_sets;
+  const int64_t total = total_tiles<TT>(a);
+  const int64_t per = tiles_per_cta(total, ctas);
+  int64_t seq, base, item, n;
+  if (by_item) {
+    seq = blockIdx.x / items_per_seq;
+    item = blockIdx.x - seq * items_per_seq;
+    n = item_tiles<TT>(a, seq);
+    int64_t sum = 0;
+    for (int64_t b = threadIdx.x & 31; b < seq; b += 32) sum += item_tiles<TT>(a, b);
+    base = warp_sum_i64(sum) * items_per_seq;
+  } else {
+    const int64_t x = per * (static_cast<int64_t>(blockIdx.x) + 1);
+    if (x >= total) return;
+    find_sequence<TT>(a, x, seq, base);
+    n = item_tiles<TT>(a, seq);
+    item = (x - base) / n;
+  }
+  const int64_t begin = base + item * n;
+  const int64_t c0 = begin / per, c1 = (begin + n - 1) / per;
+  if (c0 == c1 || (!by_item && c0 != static_cast<int64_t>(blockIdx.x))) return;
+  const int kvh = static_cast<int>(item / a.head_sets);
+  const int set = static_cast<int>(item - static_cast<int64_t>(kvh) * a.head_sets);
+  const int heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
+  const int vec = threadIdx.x % kVec, split = threadIdx.x / kVec;
+
+  for (int h = blockIdx.y; h < heads; h += gridDim.y) {
+    float top = -INFINITY, sum_l = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int64_t c = c0 + split; c <= c1; c += kSplit) {
+      const float* part = a.parts + (c * 2 + (c == c0 ? 1 : 0)) * static_cast<int64_t>(Shape::kPartFloats);
+      const float2 st = *reinterpret_cast<const float2*>(part + kHeads * D + 2 * h);
+      const float4 v = *reinterpret_cast<const float4*>(part + h * D + 4 * vec);
+      const float next = fmaxf(top, st.x);
+      const float keep = top == next ? 1.0f : exp2f(top - next), f = st.x == next ? 1.0f : exp2f(st.x - next);
+      sum_l = fmaf(st.y, f, sum_l * keep);
+      sum.x = fmaf(v.x, f, sum.x * keep);
+      sum.y = fmaf(v.y, f, sum.y * keep);
+      sum.z = fmaf(v.z, f, sum.z * keep);
+      sum.w = fmaf(v.w, f, sum.w * keep);
+      top = next;
+    }
+    __syncthreads();  // the previous head's readers are done
+    *reinterpret_cast<float4*>(&s_o[split][4 * vec]) = sum;
+    if (vec == 0) {
+      s_m[split] = top;
+      s_l[split] = sum_l;
+    }
+    __syncthreads();
+    const int64_t at = seq * a.q_heads + kvh * a.group + set * kHeads + h;
+    float all = -INFINITY, total_l = 0.0f, f[kSplit];
+#pragma unroll
+    for (int p = 0; p < kSplit; ++p) all = fmaxf(all, s_m[p]);
+#pragma unroll
+    for (int p = 0; p < kSplit; ++p) {
+      f[p] = s_m[p] == all ? 1.0f : exp2f(s_m[p] - all);
+      total_l = fmaf(s_l[p], f[p], total_l);
+    }
+    for (int c = threadIdx.x; c < D; c += kPagedThreads) {
+      float r = 0.0f;
+#pragma unroll
+      for (int p = 0; p < kSplit; ++p) r = fmaf(s_o[p][c], f[p], r);
+      static_cast<T*>(a.out)[at * D + c] = static_cast<T>(r / total_l);
+    }
+    if (threadIdx.x == 0 && a.lse != nullptr)
+      a.lse[at] = ((all == -INFINITY ? 0.0f : all) - kLift + log2f(total_l)) * kLn2;
+  }
+}
+
+}  // namespace dq
