@@ -149,10 +149,13 @@ def test_helpers_check_tensors_on_the_host(dq_lib):
     with pytest.raises(ValueError, match="q_weight"):
         d.qk_norm_rope(q, k, pos, freq, torch.ones(32))
     with pytest.raises(ValueError, match="densely"):
-        d._head_rows("q", q.transpose(1, 2))
+        d._row_stride("q", q.transpose(1, 2))
+    with pytest.raises(ValueError, match="overlap"):
+        d._row_stride("q", torch.zeros(1, 8, 64).expand(4, 8, 64))
     with pytest.raises(ValueError, match="densely"):
-        d._head_rows("q", torch.zeros(1, 8, 64).expand(4, 8, 64))
-    assert d._head_rows("q", torch.zeros(4, 12, 64)[:, 2:10])[1] == 12 * 64
+        d._row_stride("q", torch.zeros(4, 8, 128)[:, :, :64])
+    assert d._row_stride("q", torch.zeros(4, 12, 64)[:, 2:10]) == 12 * 64
+    assert d._row_stride("q", torch.zeros(1, 12, 64)[:, 2:10]) == 8 * 64
     a, b = torch.zeros(4, 32, dtype=torch.int8), torch.zeros(8, 32, dtype=torch.int8)
     with pytest.raises(ValueError, match="activation"):
         d.w8a8_linear(a, b, torch.ones(4), torch.ones(8), activation="tanh")
@@ -165,14 +168,28 @@ def test_helpers_check_tensors_on_the_host(dq_lib):
     with pytest.raises(ValueError, match="CUDA"):
         d.w8a8_linear(a, b, torch.ones(4), torch.ones(8))
     cache = torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+    codes, scales = cache.to(torch.int8), torch.ones(3, 2, 16)
+    table, lengths = torch.zeros(4, 2, dtype=torch.int32), torch.ones(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
-        d.paged_attention(q, cache, cache, torch.zeros(4, 2, dtype=torch.int32), torch.ones(4, dtype=torch.int32))
-    with pytest.raises(TypeError, match="k_cache"):
-        d._cache_tensors(cache.half(), cache, None, None, 2, 64, torch.bfloat16, q.device)
-    with pytest.raises(ValueError, match="v_cache"):
-        d._cache_tensors(cache, cache[:2], None, None, 2, 64, torch.bfloat16, q.device)
-    with pytest.raises(ValueError, match="needs k_scale"):
-        d._cache_tensors(cache.to(torch.int8), cache.to(torch.int8), None, None, 2, 64, torch.bfloat16, q.device)
-    with pytest.raises(ValueError, match="v_scale"):
-        d._cache_tensors(cache.to(torch.int8), cache.to(torch.int8), torch.ones(3, 2, 16), torch.ones(3, 2, 8), 2, 64,
-                         torch.bfloat16, q.device)
+        d.paged_attention(q, cache, cache, table, lengths)
+    for kw, error, match in [
+        (dict(k_cache=cache.half()), TypeError, "k_cache"), (dict(v_cache=cache[:2]), ValueError, "v_cache"),
+        (dict(k_cache=codes, v_cache=codes), ValueError, "needs k_scale"),
+        (dict(k_cache=codes, v_cache=codes, k_scale=scales, v_scale=scales[:, :, :8]), ValueError, "v_scale"),
+        (dict(k_cache=codes, v_cache=codes, k_scale=scales, v_scale=scales.half()), TypeError, "v_scale"),
+        (dict(page_table=table.long()), TypeError, "page_table"), (dict(page_table=table[:3]), ValueError, "page_table"),
+        (dict(lengths=lengths[:3]), ValueError, "lengths"), (dict(lse=torch.ones(4, 2)), ValueError, "lse"),
+        (dict(out=torch.ones(4, 8, 64)), TypeError, "out"), (dict(q=q[:, :, :32]), ValueError, "k_cache"),
+        (dict(k_cache=cache.transpose(0, 2)), ValueError, "k_cache"),
+    ]:
+        with pytest.raises(error, match=match):
+            d.paged_attention(**{**dict(q=q, k_cache=cache, v_cache=cache, page_table=table, lengths=lengths), **kw})
+    slots = torch.arange(4)
+    base = dict(q=q, k=k, v=k, positions=pos, inv_freq=freq, slots=slots, k_cache=cache, v_cache=cache)
+    for kw, error, match in [
+        (dict(v=k[:3]), ValueError, "v must"), (dict(slots=slots.int()), TypeError, "slots"),
+        (dict(slots=slots[:2]), ValueError, "slots"), (dict(k_cache=cache[:, :1]), ValueError, "k_cache"),
+        (dict(out=q.half()), TypeError, "out"), (dict(inv_freq=freq.double()), TypeError, "inv_freq"), ({}, ValueError, "CUDA"),
+    ]:
+        with pytest.raises(error, match=match):
+            d.qk_norm_rope_cache(**{**base, **kw})

@@ -44,16 +44,28 @@ constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the running 
 constexpr float kLift = 6.0f;   // log2 of the weight at the running maximum
 constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;
 
+#ifndef PA_TT8
+#define PA_TT8 16
+#endif
+#ifndef PA_CTAS
+#define PA_CTAS 4
+#endif
 template <typename C, int D, int HT>
 struct PagedShape {
   static constexpr bool kCodes = sizeof(C) == 1;
-  // 4 KB of K and of V in flight per warp, a multiple of 16 tokens, at most one token per lane
-  static constexpr int kFit = 4096 / (D * int(sizeof(C)));
-  static constexpr int kTokens = kFit >= 32 ? 32 : 16;
+  static constexpr int kTokens = kCodes && D <= 128 ? PA_TT8 : 16;
   static constexpr int kHeads = 8 * HT;
   // one CTA's parts: O [kHeads][D], then (max, sum) [kHeads]
   static constexpr int kPartFloats = kHeads * D + 2 * kHeads;
-  static constexpr size_t kSmem = size_t(kPagedWarps) * (kHeads * D + 2 * kHeads) * 4;
+  static constexpr int kCtas = HT * D > 128 ? 2 : PA_CTAS;  // CTAs per SM
+  // a warp's ring: K rows, V rows and scales of kStages tiles
+  static constexpr int kRowBytes = kTokens * D * int(sizeof(C));
+  static constexpr int kStageBytes = 2 * kRowBytes + (kCodes ? 2 * 4 * kTokens : 0);
+  static constexpr int kFit = (224 * 1024 / kCtas - 1024) / kPagedWarps / kStageBytes;
+  static constexpr int kStages = kFit < 2 ? 2 : (kFit > 8 ? 8 : kFit);
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr int kJoin = (kHeads * D + 2 * kHeads) * 4;
+  static constexpr size_t kSmem = size_t(kPagedWarps) * (kRing > kJoin ? kRing : kJoin);
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
@@ -96,14 +108,29 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Asynchronous copies into shared memory; `from` bytes are read, the rest is zero.
 template <int BYTES>
-__device__ __forceinline__ void load_piece(uint32_t (&r)[BYTES / 4], const void* p) {
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int from) {
   if constexpr (BYTES == 16) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p));
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
+  } else if constexpr (BYTES == 8) {
+    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
   } else {
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "l"(p));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
+  }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int BYTES>
+__device__ __forceinline__ void load_piece(uint32_t (&r)[BYTES / 4], uint32_t addr) {
+  if constexpr (BYTES == 16) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+  } else {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
   }
 }
 
@@ -168,7 +195,7 @@ __device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int64_t ctas) {
 // ---------------------------------------------------------------- main kernel
 
 template <typename T, typename C, int D, int HT>
-__global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) paged_attention_mma_kernel(const PagedArgs a) {
   using Shape = PagedShape<C, D, HT>;
   constexpr bool kCodes = Shape::kCodes;
   constexpr bool kBf16 = !kCodes && sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
@@ -180,7 +207,8 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(cons
   constexpr int kVPiece = kVBytes / kElem;   // elements of a V piece
   constexpr int VP = D / (8 * kVPiece);      // V pieces per lane and row
   constexpr int KS = D / 16;                 // k-steps of S, and row tiles of O^T
-  extern __shared__ float smem[];            // [warps][kHeads][D], [warps][kHeads][2]
+  constexpr int kStages = Shape::kStages;
+  extern __shared__ __align__(128) float smem[];  // the warps' rings; then [warps][kHeads][D], [warps][kHeads][2]
   float* s_o = smem;
   float* s_stat = smem + kPagedWarps * kHeads * D;
 
@@ -292,64 +320,74 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(cons
                  static_cast<uint32_t>(a.page_size) + in_page;
     };
 
-    uint32_t kr[MT][2][KP][4];                   // K pieces of rows g and g + 8
-    uint32_t vr[MT][4][VP][kVBytes / 4];         // V pieces of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-    uint32_t krow[MT][2];                        // cache rows of tokens g and g + 8
-    float ks[MT][2], vs[MT][2];
-    const auto load_k = [&](uint32_t row) {
+    // a stage: K pieces [MT][2][KP][lane], V pieces [MT][4][VP][lane], K scales, V scales [TT]
+    const auto issue = [&](uint32_t stage, uint32_t row) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * mt + 8 * h + g);
-          krow[mt][h] = r;
-          const bool on = r < kRowBad;
-          const C* p = static_cast<const C*>(a.k_cache) + static_cast<uint64_t>(r) * D + kPiece * t;
+          const uint32_t dst = stage + (mt * 2 + h) * KP * 512 + lane * 16;
+          const C* p = static_cast<const C*>(a.k_cache) + (r < kRowBad ? static_cast<uint64_t>(r) * D : 0u) + kPiece * t;
+          if (kCodes || r != kRowBad) {
 #pragma unroll
-          for (int i = 0; i < KP; ++i) {
-            if (on) {
-              load_piece<16>(kr[mt][h][i], p + 4 * kPiece * i);
-            } else {
-              kr[mt][h][i][0] = kr[mt][h][i][1] = kr[mt][h][i][2] = kr[mt][h][i][3] = 0u;
-            }
-          }
-          if constexpr (kCodes) {
-            ks[mt][h] = on ? __ldg(a.k_scale + r) : 0.0f;
-            vs[mt][h] = on ? __ldg(a.v_scale + r) : 0.0f;
+            for (int i = 0; i < KP; ++i) copy_async<16>(dst + i * 512, p + 4 * kPiece * i, r < kRowBad ? 16 : 0);
+          } else {  // NaN keys: the sequence's rows become NaN
+#pragma unroll
+            for (int i = 0; i < KP; ++i)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * 512), "r"(0x7FFF7FFFu) : "memory");
           }
         }
       }
-    };
-    const auto load_v = [&](uint32_t row) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1));
-          const C* p = static_cast<const C*>(a.v_cache) + static_cast<uint64_t>(r) * D + kVPiece * g;
+          const uint32_t dst = stage + Shape::kRowBytes + (mt * 4 + k) * VP * 32 * kVBytes + lane * kVBytes;
+          const C* p = static_cast<const C*>(a.v_cache) + (r < kRowBad ? static_cast<uint64_t>(r) * D : 0u) + kVPiece * g;
 #pragma unroll
-          for (int i = 0; i < VP; ++i) {
-            if (r < kRowBad) {
-              load_piece<kVBytes>(vr[mt][k][i], p + 8 * kVPiece * i);
-            } else {
-#pragma unroll
-              for (int w = 0; w < kVBytes / 4; ++w) vr[mt][k][i][w] = 0u;
-            }
+          for (int i = 0; i < VP; ++i)
+            copy_async<kVBytes>(dst + i * 32 * kVBytes, p + 8 * kVPiece * i, r < kRowBad ? kVBytes : 0);
+        }
+      }
+      if constexpr (kCodes) {
+        if (lane < TT) {
+          const uint32_t dst = stage + 2 * Shape::kRowBytes + lane * 4;
+          const uint32_t r = row < kRowBad ? row : 0u;
+          copy_async<4>(dst + TT * 4, a.v_scale + r, row < kRowBad ? 4 : 0);
+          if (row != kRowBad) {
+            copy_async<4>(dst, a.k_scale + r, row < kRowBad ? 4 : 0);
+          } else {
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(0x7FFFFFFFu) : "memory");
           }
         }
       }
+      copies_commit();
     };
 
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * Shape::kRing;
     int tl = t0 + warp;
-    uint32_t in_page = 0u, in_page_next = 0u;
-    int32_t page = find_page(tl, in_page);
-    uint32_t row = row_of(page, in_page);
-    int32_t page_next = find_page(tl + kPagedWarps, in_page_next);
-    if (tl < t1) {
-      load_k(row);
-      load_v(row);
+    __syncthreads();  // the previous item's readers of the shared memory are done
+    {
+      int32_t page[kStages];
+      uint32_t in_page[kStages];
+#pragma unroll
+      for (int st = 0; st < kStages; ++st) page[st] = find_page(tl + st * kPagedWarps, in_page[st]);
+#pragma unroll
+      for (int st = 0; st < kStages; ++st) {
+        if (tl + st * kPagedWarps < t1) {
+          issue(ring + st * Shape::kStageBytes, row_of(page[st], in_page[st]));
+        } else {
+          copies_commit();
+        }
+      }
     }
+    uint32_t in_page_next = 0u, stage = ring;
+    int32_t page_next = find_page(tl + kStages * kPagedWarps, in_page_next);
     for (; tl < t1; tl += kPagedWarps) {
+      copies_wait<kStages - 1>();
+      __syncwarp();
       // ---- S^T = K Q^T
       float s[HT][MT][4];
 #pragma unroll
@@ -361,10 +399,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(cons
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
+          uint32_t k0[4], k1[4];  // rows g and g + 8
+          load_piece<16>(k0, stage + ((mt * 2) * KP + i) * 512 + lane * 16);
+          load_piece<16>(k1, stage + ((mt * 2 + 1) * KP + i) * 512 + lane * 16);
           if constexpr (kCodes) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              const uint32_t w0 = kr[mt][0][i][u] ^ 0x80808080u, w1 = kr[mt][1][i][u] ^ 0x80808080u;
+              const uint32_t w0 = k0[u] ^ 0x80808080u, w1 = k1[u] ^ 0x80808080u;
               const uint32_t a0 = codes_f16(w0, 0x4140u), a2 = codes_f16(w0, 0x4342u);
               const uint32_t a1 = codes_f16(w1, 0x4140u), a3 = codes_f16(w1, 0x4342u);
 #pragma unroll
@@ -376,42 +417,40 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(cons
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht)
-                mma16816<kBf16>(s[ht][mt], kr[mt][0][i][2 * u], kr[mt][1][i][2 * u], kr[mt][0][i][2 * u + 1],
-                                kr[mt][1][i][2 * u + 1], qf[ht][2 * i + u][0], qf[ht][2 * i + u][1]);
+                mma16816<kBf16>(s[ht][mt], k0[2 * u], k1[2 * u], k0[2 * u + 1], k1[2 * u + 1], qf[ht][2 * i + u][0],
+                                qf[ht][2 * i + u][1]);
             }
           }
         }
       }
       // ---- scores in log2, hidden tokens out
       float vw[MT][2];
-      bool hidden[MT][2];
       bool move = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          hidden[mt][h] = krow[mt][h] == kRowHidden;
-          const bool bad = krow[mt][h] == kRowBad;
-          vw[mt][h] = kCodes ? vs[mt][h] : 1.0f;
-          if (kCodes) move |= vs[mt][h] > v_top;
+          const int tok = 16 * mt + 8 * h + g;
+          const bool hidden = static_cast<uint32_t>(tl) * TT + tok >= count;
+          float k_mul = 1.0f;
+          vw[mt][h] = 1.0f;
+          if constexpr (kCodes) {
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k_mul) : "r"(stage + 2 * Shape::kRowBytes + tok * 4));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vw[mt][h]) : "r"(stage + 2 * Shape::kRowBytes + (TT + tok) * 4));
+            move |= vw[mt][h] > v_top;
+          }
 #pragma unroll
           for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               float& x = s[ht][mt][2 * h + c];
-              x *= kCodes ? ks[mt][h] * q_mul[ht][c] : q_mul[ht][c];
-              if (hidden[mt][h]) x = -INFINITY;
-              if (bad) x = NAN;
+              x *= kCodes ? k_mul * q_mul[ht][c] : q_mul[ht][c];
+              if (hidden) x = -INFINITY;
               move |= x > m[ht][c] + kSlack;
             }
           }
         }
       }
-      // ---- the next tile's K, its table entries already here
-      row = row_of(page_next, in_page_next);
-      page_next = find_page(tl + 2 * kPagedWarps, in_page_next);
-      const bool more = tl + kPagedWarps < t1;
-      if (more) load_k(row);
       // ---- the running maximum and the largest value scale, when they have to move
       if (__any_sync(0xffffffffu, move)) {
         float v_keep = 1.0f;
@@ -487,9 +526,13 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(cons
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int i = 0; i < VP; ++i) {
+          uint32_t vr[4][kVBytes / 4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            load_piece<kVBytes>(vr[k], stage + Shape::kRowBytes + ((mt * 4 + k) * VP + i) * 32 * kVBytes + lane * kVBytes);
 #pragma unroll
           for (int w = 0; w < kVBytes / 4; ++w) {
-            const uint32_t va = vr[mt][0][i][w], vb = vr[mt][1][i][w], vc = vr[mt][2][i][w], vd = vr[mt][3][i][w];
+            const uint32_t va = vr[0][w], vb = vr[1][w], vc = vr[2][w], vd = vr[3][w];
             if constexpr (kCodes) {  // four channels of two tokens pairs: two row tiles
               const int tile0 = (i * (kVBytes / 4) + w) * 2;
               const uint32_t ab01 = prmt(va, vb, 0x5140u) ^ 0x80808080u, ab23 = prmt(va, vb, 0x7362u) ^ 0x80808080u;
@@ -515,12 +558,21 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_mma_kernel(cons
           }
         }
       }
-      if (more) load_v(row);
+      // ---- refill the stage; its table entries were asked for one tile ago
+      __syncwarp();
+      if (tl + kStages * kPagedWarps < t1) {
+        issue(stage, row_of(page_next, in_page_next));
+      } else {
+        copies_commit();
+      }
+      page_next = find_page(tl + (kStages + 1) * kPagedWarps, in_page_next);
+      stage = stage + Shape::kStageBytes == ring + Shape::kRing ? ring : stage + Shape::kStageBytes;
     }
+    copies_wait<0>();
 
     // ---- join the warps
     const float v_undo = 1.0f / v_mul;
-    __syncthreads();  // the previous item's readers are done
+    __syncthreads();  // every warp is done with its ring
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll

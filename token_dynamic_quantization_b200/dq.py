@@ -14,7 +14,6 @@ missing; there is no fallback path.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -408,59 +407,78 @@ def w8a8_gemm(a, b, a_scale, b_scale, out_dtype=None, out=None, accumulate: bool
     return out
 
 
-# The helpers below check every tensor's shape, type and device on the host:
-# the kernels index by the sizes they are given. The launch goes to the
+# The helpers below check every tensor's shape, type, layout and device on the
+# host: the kernels index by the sizes they are given. The launch goes to the
 # tensors' device whatever the current one is, on that device's current stream
 # or on `stream` (a cudaStream_t); what a helper allocates is allocated for that
 # stream, so the allocator does not hand it on while the kernel still uses it.
+# They are called once per layer and token, so each tensor is looked at in one
+# call and the C entry point is called directly.
 
 _ACTIVATIONS = {None: DQ_ACT_NONE, "none": DQ_ACT_NONE, "relu": DQ_ACT_RELU, "gelu": DQ_ACT_GELU,
                 "gelu_tanh": DQ_ACT_GELU_TANH, "silu": DQ_ACT_SILU}
 
 
-def _on(device, stream):
-    """The context to allocate and launch in: the device current, and `stream` when one is given."""
+def _elsewhere(index: int, stream) -> bool:
+    """Whether a call has to move to another device or stream than the current ones (see _on)."""
+    return index >= 0 and (stream is not None or index != _torch().cuda.current_device())
+
+
+def _on(index: int, stream):
+    """The context that makes device `index` current, and `stream` when one is given."""
     torch = _torch()
-    if stream is not None:
-        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
-                                 else torch.cuda.default_stream(device))
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if stream is None:
+        return torch.cuda.device(index)
+    device = torch.device("cuda", index)
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if stream
+                             else torch.cuda.default_stream(device))
 
 
-def _same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _stream_of(index: int) -> int:
+    """The current stream of device `index`, without the Stream object around it where torch offers that.
+
+    The last thing a helper asks before its launch: tensors on the CPU end here."""
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _expect(name: str, t, shape, dtype) -> None:
+def _arg(name: str, t, shape, dtype, index: int) -> int:
+    """The pointer of a dense tensor after checking it."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _cuda_first(t, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
-
-
-def _head_rows(name: str, t, dtype=None):
-    """[tokens, heads, head_dim] with dense heads -> (pointer, elements between tokens)."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
-    if dtype is not None and t.dtype != dtype:
+def _rows(name: str, t, shape, dtype, index: int):
+    """(pointer, elements between tokens) of [tokens, heads, head_dim] with dense heads, after checking it."""
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    return t.data_ptr(), _row_stride(name, t)
+
+
+def _row_stride(name: str, t) -> int:
     tokens, heads, dim = t.shape
     row, head, one = t.stride()
-    if t.numel() == 0:
-        return t.data_ptr(), heads * dim
-    if (dim > 1 and one != 1) or (heads > 1 and head != dim) or (tokens > 1 and row < heads * dim):
+    if t.numel() == 0 or tokens == 1:
+        row = heads * dim
+    elif row < heads * dim:
+        raise ValueError(f"{name}: tokens overlap")
+    if t.numel() and ((one != 1 and dim > 1) or (head != dim and heads > 1)):
         raise ValueError(f"{name}: the heads of a token must lie densely one after the other")
-    return t.data_ptr(), (row if tokens > 1 else heads * dim)
+    return row
 
 
 def w8a8_linear(a, b, a_scale, b_scale, bias=None, activation=None, residual=None, out_dtype=None, out=None,
@@ -476,59 +494,50 @@ def w8a8_linear(a, b, a_scale, b_scale, bias=None, activation=None, residual=Non
     torch = _torch()
     if a.dim() != 2 or b.dim() != 2 or a.dtype != torch.int8 or b.dtype != torch.int8:
         raise TypeError("a and b must be 2-D int8 tensors")
-    (m, k), n = a.shape, b.shape[0]
+    m, k = a.shape
+    n = b.shape[0]
     if b.shape[1] != k:
         raise ValueError(f"b must be [N, K] with the K of a ({k}), got {tuple(b.shape)}")
-    if activation not in _ACTIVATIONS:
+    act = _ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"unknown activation {activation!r}")
-    _expect("a_scale", a_scale, (m,), torch.float32)
-    _expect("b_scale", b_scale, (n,), torch.float32)
-    if bias is not None:
-        _expect("bias", bias, (n,), bias.dtype)
-    if out is not None:
-        out_dtype = out.dtype if out_dtype is None else out_dtype
-    elif out_dtype is None:
-        out_dtype = torch.float32 if residual is None else residual.dtype
-    if residual is not None:
-        _expect("residual", residual, (m, n), out_dtype)
-    if out is not None:
-        _expect("out", out, (m, n), out_dtype)
-    device = _cuda_first(a, "a")
-    _same_device(device, b=b, a_scale=a_scale, b_scale=b_scale, bias=bias, residual=residual, out=out)
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty((m, n), dtype=out_dtype, device=device)
-        if stream is None:
-            stream = torch.cuda.current_stream(device).cuda_stream
-        st = dq_w8a8_linear(_dev_ptr(a, "a"), _dev_ptr(b, "b"), m, n, k, _dev_ptr(a_scale, "a_scale"),
-                            _dev_ptr(b_scale, "b_scale"), _dev_ptr(bias, "bias"),
-                            DQ_F32 if bias is None else _dtype_code(bias), _ACTIVATIONS[activation],
-                            _dev_ptr(residual, "residual"), _dev_ptr(out, "out"), _dtype_code(out), stream)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else (torch.float32 if residual is None else residual.dtype)
+    index = a.get_device()
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return w8a8_linear(a, b, a_scale, b_scale, bias, activation, residual, out_dtype, out, None, check)
+    if out is None:
+        out = a.new_empty((m, n), dtype=out_dtype)
+    st = _lib.dq_w8a8_linear(
+        _arg("a", a, (m, k), torch.int8, index), _arg("b", b, (n, k), torch.int8, index), m, n, k,
+        _arg("a_scale", a_scale, (m,), torch.float32, index), _arg("b_scale", b_scale, (n,), torch.float32, index),
+        None if bias is None else _arg("bias", bias, (n,), bias.dtype, index),
+        DQ_F32 if bias is None else _dtype_code(bias), act,
+        None if residual is None else _arg("residual", residual, (m, n), out_dtype, index),
+        _arg("out", out, (m, n), out_dtype, index), _dtype_code(out), _stream_of(index))
     if check and st != DQ_OK:
         raise DQError(st)
     return out
 
 
-def _norm_rope_inputs(q, k, positions, inv_freq, q_weight, k_weight):
-    """Shared checks: (device, tokens, q_heads, kv_heads, head_dim, rope_dim, weight dtype code)."""
-    torch = _torch()
+def _weights(q_weight, k_weight, dim: int, index: int):
+    """(q_weight pointer, k_weight pointer, dtype code)."""
+    one = q_weight if q_weight is not None else k_weight
+    if one is None:
+        return None, None, DQ_F32
+    return (None if q_weight is None else _arg("q_weight", q_weight, (dim,), one.dtype, index),
+            None if k_weight is None else _arg("k_weight", k_weight, (dim,), one.dtype, index), _dtype_code(one))
+
+
+def _norm_rope_shapes(q, k):
+    """(q's shape, k's shape) of [tokens, heads, head_dim] tensors of the same tokens and head_dim."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [tokens, heads, head_dim]")
-    tokens, q_heads, dim = q.shape
-    kv_heads = k.shape[1]
-    _expect("k", k, (tokens, kv_heads, dim), q.dtype)
-    _expect("positions", positions, (tokens,), torch.int32)
-    rope_dim = 0
-    if inv_freq is not None:
-        rope_dim = 2 * inv_freq.numel()
-        _expect("inv_freq", inv_freq, (rope_dim // 2,), torch.float32)
-    weight = q_weight if q_weight is not None else k_weight
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _expect(name, w, (dim,), weight.dtype)
-    device = _cuda_first(q, "q")
-    _same_device(device, k=k, positions=positions, inv_freq=inv_freq, q_weight=q_weight, k_weight=k_weight)
-    return device, tokens, q_heads, kv_heads, dim, rope_dim, DQ_F32 if weight is None else _dtype_code(weight)
+    q_shape, k_shape = q.shape, k.shape
+    if k_shape[0] != q_shape[0] or k_shape[2] != q_shape[2]:
+        raise ValueError(f"k must be [{q_shape[0]}, kv_heads, {q_shape[2]}], got {list(k_shape)}")
+    return q_shape, k_shape
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, epsilon: float = 1e-6,
@@ -542,48 +551,43 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, epsilo
     ``(q_out, k_out)``, also ``(q, k)`` themselves. Returns ``(q_out, k_out)``.
     """
     torch = _torch()
-    device, tokens, q_heads, kv_heads, dim, rope_dim, wdt = _norm_rope_inputs(q, k, positions, inv_freq, q_weight,
-                                                                              k_weight)
-    with _on(device, stream):
-        if out is None:
-            q_out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=device)
-            k_out = torch.empty((tokens, kv_heads, dim), dtype=q.dtype, device=device)
-        else:
-            q_out, k_out = out
-            _expect("q_out", q_out, q.shape, q.dtype)
-            _expect("k_out", k_out, k.shape, q.dtype)
-            _same_device(device, q_out=q_out, k_out=k_out)
-        if stream is None:
-            stream = torch.cuda.current_stream(device).cuda_stream
-        st = dq_qk_norm_rope(*_head_rows("q", q), *_head_rows("k", k), _dtype_code(q), tokens, q_heads, kv_heads, dim,
-                             _dev_ptr(q_weight, "q_weight"), _dev_ptr(k_weight, "k_weight"), wdt, float(epsilon),
-                             _dev_ptr(positions, "positions"), _dev_ptr(inv_freq, "inv_freq"), rope_dim,
-                             1 if interleaved else 0, *_head_rows("q_out", q_out), *_head_rows("k_out", k_out), stream)
+    q_shape, k_shape = _norm_rope_shapes(q, k)
+    (tokens, q_heads, dim), kv_heads = q_shape, k_shape[1]
+    dtype, index, half = q.dtype, q.get_device(), 0 if inv_freq is None else inv_freq.numel()
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, epsilon, interleaved, out, None, check)
+    if out is None:
+        q_out, k_out = q.new_empty(q_shape), q.new_empty(k_shape)
+    else:
+        q_out, k_out = out
+    st = _lib.dq_qk_norm_rope(
+        *_rows("q", q, q_shape, dtype, index), *_rows("k", k, k_shape, dtype, index), _dtype_code(q), tokens, q_heads,
+        kv_heads, dim, *_weights(q_weight, k_weight, dim, index), epsilon,
+        _arg("positions", positions, (tokens,), torch.int32, index),
+        None if inv_freq is None else _arg("inv_freq", inv_freq, (half,), torch.float32, index), 2 * half,
+        1 if interleaved else 0, *_rows("q_out", q_out, q_shape, dtype, index),
+        *_rows("k_out", k_out, k_shape, dtype, index), _stream_of(index))
     if check and st != DQ_OK:
         raise DQError(st)
     return q_out, k_out
 
 
-def _cache_tensors(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, device):
-    """Shared checks of a paged cache: (num_pages, page_size, cache dtype code)."""
+def _cache_args(k_cache, v_cache, k_scale, v_scale, kv_heads: int, dim: int, dtype, index: int):
+    """(k pointer, v pointer, dtype code, k_scale pointer, v_scale pointer, num_pages, page_size) of a checked cache."""
     torch = _torch()
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, kv_heads, page_size, head_dim]")
     pages, page_size = k_cache.shape[0], k_cache.shape[2]
-    codes = k_cache.dtype == torch.int8
-    if not codes and k_cache.dtype != dtype:
-        raise TypeError(f"k_cache must be {dtype} or torch.int8, got {k_cache.dtype}")
-    _expect("k_cache", k_cache, (pages, kv_heads, page_size, dim), k_cache.dtype)
-    _expect("v_cache", v_cache, k_cache.shape, k_cache.dtype)
-    _same_device(device, k_cache=k_cache, v_cache=v_cache)
-    if codes:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an int8 cache needs k_scale and v_scale")
-        _expect("k_scale", k_scale, (pages, kv_heads, page_size), torch.float32)
-        _expect("v_scale", v_scale, (pages, kv_heads, page_size), torch.float32)
-        _same_device(device, k_scale=k_scale, v_scale=v_scale)
-        return pages, page_size, DQ_INT8
-    return pages, page_size, _dtype_code(k_cache)
+    shape = (pages, kv_heads, page_size, dim)
+    if k_cache.dtype != torch.int8:
+        return (_arg("k_cache", k_cache, shape, dtype, index), _arg("v_cache", v_cache, shape, dtype, index),
+                _dtype_code(k_cache), None, None, pages, page_size)
+    if k_scale is None or v_scale is None:
+        raise ValueError("an int8 cache needs k_scale and v_scale")
+    return (_arg("k_cache", k_cache, shape, torch.int8, index), _arg("v_cache", v_cache, shape, torch.int8, index),
+            DQ_INT8, _arg("k_scale", k_scale, shape[:3], torch.float32, index),
+            _arg("v_scale", v_scale, shape[:3], torch.float32, index), pages, page_size)
 
 
 def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_scale=None, v_scale=None,
@@ -598,29 +602,24 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_
     ``q`` itself. Returns ``q_out``; the caches are updated in place.
     """
     torch = _torch()
-    device, tokens, q_heads, kv_heads, dim, rope_dim, wdt = _norm_rope_inputs(q, k, positions, inv_freq, q_weight,
-                                                                              k_weight)
-    _expect("v", v, (tokens, kv_heads, dim), q.dtype)
-    _expect("slots", slots, (tokens,), torch.int64)
-    _same_device(device, v=v, slots=slots)
-    pages, page_size, cdt = _cache_tensors(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, q.dtype, device)
-    codes = cdt == DQ_INT8
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=device)
-        else:
-            _expect("out", out, q.shape, q.dtype)
-            _same_device(device, out=out)
-        if stream is None:
-            stream = torch.cuda.current_stream(device).cuda_stream
-        st = dq_qk_norm_rope_cache(*_head_rows("q", q), *_head_rows("k", k), *_head_rows("v", v), _dtype_code(q),
-                                   tokens, q_heads, kv_heads, dim, _dev_ptr(q_weight, "q_weight"),
-                                   _dev_ptr(k_weight, "k_weight"), wdt, float(epsilon),
-                                   _dev_ptr(positions, "positions"), _dev_ptr(inv_freq, "inv_freq"), rope_dim,
-                                   1 if interleaved else 0, *_head_rows("out", out), _dev_ptr(k_cache, "k_cache"),
-                                   _dev_ptr(v_cache, "v_cache"), cdt, _dev_ptr(k_scale, "k_scale") if codes else None,
-                                   _dev_ptr(v_scale, "v_scale") if codes else None, _dev_ptr(slots, "slots"), pages,
-                                   page_size, stream)
+    q_shape, k_shape = _norm_rope_shapes(q, k)
+    (tokens, q_heads, dim), kv_heads = q_shape, k_shape[1]
+    dtype, index, half = q.dtype, q.get_device(), 0 if inv_freq is None else inv_freq.numel()
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_scale, v_scale,
+                                      q_weight, k_weight, epsilon, interleaved, out, None, check)
+    if out is None:
+        out = q.new_empty(q_shape)
+    kc, vc, cdt, ks, vs, pages, page_size = _cache_args(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, index)
+    st = _lib.dq_qk_norm_rope_cache(
+        *_rows("q", q, q_shape, dtype, index), *_rows("k", k, k_shape, dtype, index),
+        *_rows("v", v, k_shape, dtype, index), _dtype_code(q), tokens, q_heads, kv_heads, dim,
+        *_weights(q_weight, k_weight, dim, index), epsilon,
+        _arg("positions", positions, (tokens,), torch.int32, index),
+        None if inv_freq is None else _arg("inv_freq", inv_freq, (half,), torch.float32, index), 2 * half,
+        1 if interleaved else 0, *_rows("out", out, q_shape, dtype, index), kc, vc, cdt, ks, vs,
+        _arg("slots", slots, (tokens,), torch.int64, index), pages, page_size, _stream_of(index))
     if check and st != DQ_OK:
         raise DQError(st)
     return out
@@ -642,47 +641,35 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale=None, v_sc
     head_dim] of q's dtype.
     """
     torch = _torch()
-    if q.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("q must be [batch, q_heads, head_dim] and k_cache [num_pages, kv_heads, page_size, head_dim]")
-    batch, q_heads, dim = q.shape
-    kv_heads = k_cache.shape[1]
-    device = _cuda_first(q, "q")
-    pages, page_size, cdt = _cache_tensors(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, q.dtype, device)
-    codes = cdt == DQ_INT8
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [batch, max_pages]")
-    max_pages = page_table.shape[1]
-    _expect("page_table", page_table, (batch, max_pages), torch.int32)
-    _expect("lengths", lengths, (batch,), torch.int32)
-    if lse is not None:
-        _expect("lse", lse, (batch, q_heads), torch.float32)
-    _same_device(device, page_table=page_table, lengths=lengths, lse=lse, workspace=workspace)
-    ws_bytes = dq_paged_attention_get_workspace_size(batch, q_heads, kv_heads, dim, cdt)
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty((batch, q_heads, dim), dtype=q.dtype, device=device)
-        else:
-            _expect("out", out, q.shape, q.dtype)
-            _same_device(device, out=out)
-        if workspace is None and ws_bytes:
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
-        if workspace is not None:
-            ws_bytes = workspace.numel() * workspace.element_size()
-        if stream is None:
-            stream = torch.cuda.current_stream(device).cuda_stream
-        st = dq_paged_attention(*_q_rows(q), _dev_ptr(k_cache, "k_cache"),
-                                _dev_ptr(v_cache, "v_cache"), cdt, _dev_ptr(k_scale, "k_scale") if codes else None,
-                                _dev_ptr(v_scale, "v_scale") if codes else None, _dev_ptr(page_table, "page_table"),
-                                _dev_ptr(lengths, "lengths"), batch, q_heads, kv_heads, dim, pages, page_size,
-                                max_pages, int(window), int(sinks),
-                                float(dim ** -0.5 if softmax_scale is None else softmax_scale), _dev_ptr(out, "out"),
-                                _dev_ptr(lse, "lse"), _dev_ptr(workspace, "workspace"), ws_bytes, stream)
+    if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("q must be [batch, q_heads, head_dim], k_cache [num_pages, kv_heads, page_size, head_dim] "
+                         "and page_table [batch, max_pages]")
+    batch, q_heads, dim = shape = q.shape
+    dtype, kv_heads, max_pages, index = q.dtype, k_cache.shape[1], page_table.shape[1], q.get_device()
+    if _elsewhere(index, stream):
+        with _on(index, stream):
+            return paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale, v_scale, softmax_scale, window,
+                                   sinks, out, lse, workspace, None, check)
+    if out is None:
+        out = q.new_empty(shape)
+    kc, vc, cdt, ks, vs, pages, page_size = _cache_args(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, index)
+    if workspace is None:
+        ws_bytes = dq_paged_attention_get_workspace_size(batch, q_heads, kv_heads, dim, cdt)
+        if ws_bytes:
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{index}")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    ptr, stride = _rows("q", q, shape, dtype, index)
+    st = _lib.dq_paged_attention(
+        ptr, _dtype_code(q), stride, kc, vc, cdt, ks, vs,
+        _arg("page_table", page_table, (batch, max_pages), torch.int32, index),
+        _arg("lengths", lengths, (batch,), torch.int32, index), batch, q_heads, kv_heads, dim, pages, page_size,
+        max_pages, window, sinks, dim ** -0.5 if softmax_scale is None else softmax_scale,
+        _arg("out", out, shape, dtype, index),
+        None if lse is None else _arg("lse", lse, (batch, q_heads), torch.float32, index),
+        None if workspace is None else workspace.data_ptr(), ws_bytes, _stream_of(index))
     if check and st != DQ_OK:
         raise DQError(st)
     return out
-
-
-def _q_rows(q):
-    """(pointer, dtype code, elements between sequences) of paged_attention's q."""
-    ptr, stride = _head_rows("q", q)
-    return ptr, _dtype_code(q), stride
