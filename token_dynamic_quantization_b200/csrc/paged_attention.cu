@@ -16,6 +16,7 @@
 #include "dq_launch.cuh"
 #include "paged_attention_args.cuh"
 #include "paged_attention_mma.cuh"
+#include "tensor_map.cuh"
 
 namespace dq {
 
@@ -137,10 +138,48 @@ size_t parts_bytes(int group, int dim) {
   return static_cast<size_t>(most_ctas()) * 2 * (heads * dim + 2 * heads) * sizeof(float);
 }
 
+// A cache as a list of rows, copied four at a time in boxes of 128 bytes (64
+// for 64 codes) with the swizzle of that width.
+template <typename C, int BOX>
+bool rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim) {
+  dq_host::EncodeTiledFn fn = dq_host::encode_tiled();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(dim) * sizeof(C)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(BOX / sizeof(C)), 1}, estride[2] = {1, 1};
+  return fn(map, sizeof(C) == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+            const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Kernel, typename... Args>
+dq_status launch_pdl(Kernel kernel, dim3 grid, size_t smem, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(dq::kPagedThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return DQ_ERR_CUDA;
+  }
+  return dq_host::launch_status();
+}
+
 template <typename T, typename C, int D, int HT>
 dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
   using Shape = dq::PagedShape<C, D, HT>;
-  void (*fn)(const dq::PagedArgs) = dq::paged_attention_mma_kernel<T, C, D, HT>;
+  auto fn = dq::paged_attention_mma_kernel<T, C, D, HT>;
+  CUtensorMap k_map, v_map;
+  const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
+  if (!rows_map<C, Shape::kBox>(&k_map, a.k_cache, rows, D) || !rows_map<C, Shape::kBox>(&v_map, a.v_cache, rows, D))
+    return dq_host::kNotLaunchable;
   const int device = dq_host::current_device();
   if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
   a.head_sets = (a.group + Shape::kHeads - 1) / Shape::kHeads;
@@ -149,25 +188,13 @@ dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
                  dq_host::blocks_per_sm(reinterpret_cast<const void*>(fn), dq::kPagedThreads, Shape::kSmem, device);
   if (ctas > most_ctas()) ctas = most_ctas();
   a.whole = 0;
-  dq_status st = dq_host::launch_programmatic(fn, a, static_cast<int>(ctas), dq::kPagedThreads, Shape::kSmem, stream);
+  const dq_status st = launch_pdl(fn, dim3(static_cast<unsigned>(ctas)), Shape::kSmem, stream, k_map, v_map, a);
   if (st != DQ_OK) return st;
   const int by_item = a.items < ctas ? 1 : 0;
   const int heads = a.group < Shape::kHeads ? a.group : Shape::kHeads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(by_item ? a.items : ctas - 1), by_item ? heads : 1);
-  cfg.blockDim = dim3(dq::kPagedThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void (*join)(const dq::PagedArgs, const int, const int) = dq::paged_attention_join_kernel<T, C, D, HT>;
-  if (cudaLaunchKernelEx(&cfg, join, a, static_cast<int>(ctas), by_item) != cudaSuccess) {
-    cudaGetLastError();
-    return DQ_ERR_CUDA;
-  }
-  return dq_host::launch_status();
+  return launch_pdl(dq::paged_attention_join_kernel<T, C, D, HT>,
+                    dim3(static_cast<unsigned>(by_item ? a.items : ctas - 1), by_item ? heads : 1), 0, stream, a,
+                    static_cast<int>(ctas), by_item);
 }
 
 template <typename T, typename C>
@@ -268,10 +295,10 @@ extern "C" dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t
   a.page_shift = shift;
   a.page_mul = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - page_size)) / page_size + 1);
   a.parts = static_cast<float*>(workspace);
-  // 16-byte pieces of cache rows, 8-byte pieces of q and out rows, row numbers below 2^32
+  // 16-byte pieces of cache rows, 8-byte pieces of q and out rows, row numbers below 2^31
   const bool mma = mma_dim(head_dim) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(q, 8) &&
                    q_stride % 4 == 0 && aligned(out, 8) &&
-                   num_pages <= int64_t(0xFFFFFFF0u) / page_size / kv_heads;
+                   num_pages <= int64_t(0x7FFFFFFF) / page_size / kv_heads;
   if (q_dtype == DQ_F16) {
     return codes ? dispatch<__half, int8_t>(a, mma, stream) : dispatch<__half, __half>(a, mma, stream);
   }

@@ -30,11 +30,13 @@
 // workspace, and a second kernel joins them.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "dq_device.cuh"
 #include "paged_attention_args.cuh"
+#include "tma_pipeline.cuh"
 
 namespace dq {
 
@@ -42,13 +44,13 @@ constexpr int kPagedWarps = 4;
 constexpr int kPagedThreads = kPagedWarps * 32;
 constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the running maximum
 constexpr float kLift = 6.0f;   // log2 of the weight at the running maximum
-constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;
+constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;  // row numbers outside every cache
 
 #ifndef PA_TT8
-#define PA_TT8 16
+#define PA_TT8 32
 #endif
 #ifndef PA_CTAS
-#define PA_CTAS 4
+#define PA_CTAS 3
 #endif
 template <typename C, int D, int HT>
 struct PagedShape {
@@ -58,14 +60,21 @@ struct PagedShape {
   // one CTA's parts: O [kHeads][D], then (max, sum) [kHeads]
   static constexpr int kPartFloats = kHeads * D + 2 * kHeads;
   static constexpr int kCtas = HT * D > 128 ? 2 : PA_CTAS;  // CTAs per SM
-  // a warp's ring: K rows, V rows and scales of kStages tiles
+  // rows lie in shared memory in boxes of 128 bytes (64 for 64 codes), swizzled
+  static constexpr int kBox = D * int(sizeof(C)) < 128 ? D * int(sizeof(C)) : 128;
+  static constexpr int kBoxes = D * int(sizeof(C)) / kBox;
+  // a warp's ring: K and V boxes of kStages tiles, then the tiles' scales
   static constexpr int kRowBytes = kTokens * D * int(sizeof(C));
-  static constexpr int kStageBytes = 2 * kRowBytes + (kCodes ? 2 * 4 * kTokens : 0);
-  static constexpr int kFit = (224 * 1024 / kCtas - 1024) / kPagedWarps / kStageBytes;
+  static constexpr int kScaleBytes = kCodes ? 2 * 4 * kTokens : 0;
+  static constexpr int kStageBytes = 2 * kRowBytes;
+  static constexpr int kFit = (224 * 1024 / kCtas - 2048) / kPagedWarps / (kStageBytes + kScaleBytes);
   static constexpr int kStages = kFit < 2 ? 2 : (kFit > 8 ? 8 : kFit);
-  static constexpr int kRing = kStages * kStageBytes;
-  static constexpr int kJoin = (kHeads * D + 2 * kHeads) * 4;
-  static constexpr size_t kSmem = size_t(kPagedWarps) * (kRing > kJoin ? kRing : kJoin);
+  static constexpr int kRings = kPagedWarps * kStages * kStageBytes;
+  static constexpr int kScales = kPagedWarps * kStages * kScaleBytes;
+  static constexpr int kJoin = kPagedWarps * (kHeads * D + 2 * kHeads) * 4;
+  static constexpr int kBarriers = kPagedWarps * kStages * 8;
+  static constexpr int kBody = kRings + kScales > kJoin ? kRings + kScales : kJoin;
+  static constexpr size_t kSmem = 1024 + size_t(kBody) + kBarriers;  // 1024: alignment of the swizzle pattern
 };
 
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) { return __byte_perm(a, b, sel); }
@@ -100,24 +109,29 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two codes, biased by 128 in bytes `sel` of w, as exact f16 values.
-__device__ __forceinline__ uint32_t codes_f16(uint32_t w, uint32_t sel) {
-  const uint32_t h = prmt(w, 0x64646464u, sel);
-  const uint32_t bias = 0x64806480u;  // 1152
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// Two bytes of w as f16: a byte in the low bits of an f16 is the subnormal byte *
+// 2^-24, exact in the products.
+__device__ __forceinline__ uint32_t bytes_f16(uint32_t w, uint32_t sel) { return prmt(w, 0u, sel); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// Asynchronous copies into shared memory; `from` bytes are read, the rest is zero.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int from) {
-  if constexpr (BYTES == 16) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
-  } else if constexpr (BYTES == 8) {
-    asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
-  } else {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
-  }
+// Four rows of a tensor map, `x` elements into each, one after the other to
+// `dst`; a row outside the map is filled with zeros.
+__device__ __forceinline__ void gather_rows(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, int from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(from) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -132,6 +146,28 @@ __device__ __forceinline__ void load_piece(uint32_t (&r)[BYTES / 4], uint32_t ad
   } else {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
   }
+}
+
+// Offset of 16-byte piece `piece` of row `row` in a stage's boxes, as the
+// copies' swizzle lays them: within 128-byte rows the piece's number is XORed
+// with the row's low three bits, within 64-byte rows with bits 1 and 2.
+template <typename Shape, int TT>
+__device__ __forceinline__ uint32_t box_offset(int row, int piece) {
+  if constexpr (Shape::kBox == 128) {
+    return (piece >> 3) * TT * 128 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+  } else {
+    return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+  }
+}
+
+// Which of 8 tokens stands at place i of the products. In 128-byte rows, 8
+// lanes of a 16-byte K load hold places 2j and 2j + 1, pieces 0-3: tokens whose
+// numbers differ in bit 2 put them into different halves of the banks. The V
+// load's 8 lanes hold places 0, 2, 4, 6 (or the odd ones), two pieces each:
+// tokens that differ in bits 1 and 2.
+template <int BOX>
+__device__ __forceinline__ int token_order(int i) {
+  return BOX == 128 ? (0x37156240u >> (4 * i)) & 7 : i;
 }
 
 // ---------------------------------------------------------------- the schedule
@@ -195,7 +231,8 @@ __device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int64_t ctas) {
 // ---------------------------------------------------------------- main kernel
 
 template <typename T, typename C, int D, int HT>
-__global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) paged_attention_mma_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) paged_attention_mma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                               const PagedArgs a) {
   using Shape = PagedShape<C, D, HT>;
   constexpr bool kCodes = Shape::kCodes;
   constexpr bool kBf16 = !kCodes && sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
@@ -208,14 +245,23 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
   constexpr int VP = D / (8 * kVPiece);      // V pieces per lane and row
   constexpr int KS = D / 16;                 // k-steps of S, and row tiles of O^T
   constexpr int kStages = Shape::kStages;
-  extern __shared__ __align__(128) float smem[];  // the warps' rings; then [warps][kHeads][D], [warps][kHeads][2]
-  float* s_o = smem;
-  float* s_stat = smem + kPagedWarps * kHeads * D;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // the warps' rings and scales; once they are read, [warps][kHeads][D] and [warps][kHeads][2]
+  float* s_o = reinterpret_cast<float*>(smem);
+  float* s_stat = s_o + kPagedWarps * kHeads * D;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * kStages * Shape::kStageBytes;
+  const uint32_t scales = smem_addr(smem) + Shape::kRings + warp * kStages * Shape::kScaleBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::kBody) + warp * kStages;
+  if (lane < kStages) mbar_init(bars + lane, 1);
+  fence_mbarrier_init();
+  __syncwarp();
+  uint32_t filled = 0u;  // bit st: parity of stage st's next completion
 
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
 
   int64_t seq, base, tile, tile_end;
   const int64_t items_per_seq = static_cast<int64_t>(a.kv_heads) * a.head_sets;
@@ -234,6 +280,10 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     find_sequence<TT>(a, tile, seq, base);
   }
   const int64_t range_begin = tile;
+  // tokens of a tile in the order that spreads them over the banks: lane g's K
+  // row, and the rows of a lane's V tokens
+  const int order = token_order<Shape::kBox>(g), order_even = token_order<Shape::kBox>(2 * t);
+  const int order_odd = token_order<Shape::kBox>(2 * t + 1);
 
   while (tile < tile_end) {
     const Visible vis = visible_tokens(a, seq);
@@ -252,6 +302,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     // Q as B operands: head g, four channels per k-step
     uint32_t qf[HT][KS][2];
     float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
+    float s_init[HT][2];  // what the codes' bias of 128 adds to their products, negated
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       const bool on = 8 * ht + g < heads;
@@ -289,16 +340,35 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         }
         mul = scalbnf(mul, -e);
       }
+      float init = 0.0f;
+      if constexpr (kCodes) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[ht][s][i]));
+            init -= f.x + f.y;
+          }
+        }
+        init += __shfl_xor_sync(0xffffffffu, init, 1);
+        init += __shfl_xor_sync(0xffffffffu, init, 2);
+        init *= 0x1p-17f;  // 128 * 2^-24
+        mul *= 0x1p24f;
+      }
+      s_init[ht][0] = __shfl_sync(0xffffffffu, init, 8 * t);
+      s_init[ht][1] = __shfl_sync(0xffffffffu, init, 8 * t + 4);
       q_mul[ht][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
       q_mul[ht][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
     }
 
     float o[HT][KS][4], m[HT][2], l[HT][2];
+    float o_bias[HT][4];  // what the codes' bias of 128 has added to every channel of O
     float v_top = 0.0f, v_mul = 1.0f;  // largest value scale so far, and the power of two that takes it below 2
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       m[ht][0] = m[ht][1] = -INFINITY;
       l[ht][0] = l[ht][1] = 0.0f;
+      o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.0f;
     }
@@ -320,94 +390,84 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
                  static_cast<uint32_t>(a.page_size) + in_page;
     };
 
-    // a stage: K pieces [MT][2][KP][lane], V pieces [MT][4][VP][lane], K scales, V scales [TT]
-    const auto issue = [&](uint32_t stage, uint32_t row) {
+    bool broken = false;  // a page outside the cache, or a copy that never came: the rows become NaN
+    const auto issue = [&](int st, uint32_t row) {
+      broken |= row == kRowBad;
+      const uint32_t r0 = __shfl_sync(0xffffffffu, row, (4 * lane) & 31), r1 = __shfl_sync(0xffffffffu, row, (4 * lane + 1) & 31);
+      const uint32_t r2 = __shfl_sync(0xffffffffu, row, (4 * lane + 2) & 31), r3 = __shfl_sync(0xffffffffu, row, (4 * lane + 3) & 31);
+      const uint32_t bar = smem_addr(bars + st);
+      if (lane == 0) mbar_arrive_expect_tx(bars + st, Shape::kStageBytes);
+      __syncwarp();
+      if (lane < TT / 4) {
+        const uint32_t dst = ring + st * Shape::kStageBytes + lane * 4 * Shape::kBox;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * mt + 8 * h + g);
-          const uint32_t dst = stage + (mt * 2 + h) * KP * 512 + lane * 16;
-          const C* p = static_cast<const C*>(a.k_cache) + (r < kRowBad ? static_cast<uint64_t>(r) * D : 0u) + kPiece * t;
-          if (kCodes || r != kRowBad) {
-#pragma unroll
-            for (int i = 0; i < KP; ++i) copy_async<16>(dst + i * 512, p + 4 * kPiece * i, r < kRowBad ? 16 : 0);
-          } else {  // NaN keys: the sequence's rows become NaN
-#pragma unroll
-            for (int i = 0; i < KP; ++i)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * 512), "r"(0x7FFF7FFFu) : "memory");
-          }
-        }
-      }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t r = __shfl_sync(0xffffffffu, row, 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1));
-          const uint32_t dst = stage + Shape::kRowBytes + (mt * 4 + k) * VP * 32 * kVBytes + lane * kVBytes;
-          const C* p = static_cast<const C*>(a.v_cache) + (r < kRowBad ? static_cast<uint64_t>(r) * D : 0u) + kVPiece * g;
-#pragma unroll
-          for (int i = 0; i < VP; ++i)
-            copy_async<kVBytes>(dst + i * 32 * kVBytes, p + 8 * kVPiece * i, r < kRowBad ? kVBytes : 0);
+        for (int x = 0; x < Shape::kBoxes; ++x) {
+          gather_rows(dst + x * TT * Shape::kBox, &k_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
+          gather_rows(dst + Shape::kRowBytes + x * TT * Shape::kBox, &v_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
         }
       }
       if constexpr (kCodes) {
         if (lane < TT) {
-          const uint32_t dst = stage + 2 * Shape::kRowBytes + lane * 4;
+          const uint32_t dst = scales + st * Shape::kScaleBytes + lane * 4;
           const uint32_t r = row < kRowBad ? row : 0u;
-          copy_async<4>(dst + TT * 4, a.v_scale + r, row < kRowBad ? 4 : 0);
-          if (row != kRowBad) {
-            copy_async<4>(dst, a.k_scale + r, row < kRowBad ? 4 : 0);
-          } else {
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst), "r"(0x7FFFFFFFu) : "memory");
-          }
+          copy_async4(dst, a.k_scale + r, row < kRowBad ? 4 : 0);
+          copy_async4(dst + TT * 4, a.v_scale + r, row < kRowBad ? 4 : 0);
         }
+        copies_commit();
       }
-      copies_commit();
     };
 
-    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * Shape::kRing;
-    int tl = t0 + warp;
+    int tl = t0 + warp, st = 0;
+    fence_proxy_async_smem();
     __syncthreads();  // the previous item's readers of the shared memory are done
+    fence_proxy_async_smem();
     {
       int32_t page[kStages];
       uint32_t in_page[kStages];
 #pragma unroll
-      for (int st = 0; st < kStages; ++st) page[st] = find_page(tl + st * kPagedWarps, in_page[st]);
+      for (int i = 0; i < kStages; ++i) page[i] = find_page(tl + i * kPagedWarps, in_page[i]);
 #pragma unroll
-      for (int st = 0; st < kStages; ++st) {
-        if (tl + st * kPagedWarps < t1) {
-          issue(ring + st * Shape::kStageBytes, row_of(page[st], in_page[st]));
-        } else {
+      for (int i = 0; i < kStages; ++i) {
+        if (tl + i * kPagedWarps < t1) {
+          issue(i, row_of(page[i], in_page[i]));
+        } else if constexpr (kCodes) {
           copies_commit();
         }
       }
     }
-    uint32_t in_page_next = 0u, stage = ring;
+    uint32_t in_page_next = 0u;
     int32_t page_next = find_page(tl + kStages * kPagedWarps, in_page_next);
     for (; tl < t1; tl += kPagedWarps) {
-      copies_wait<kStages - 1>();
+      const uint32_t stage = ring + st * Shape::kStageBytes;
+      if (!mbar_wait_parity(bars + st, (filled >> st) & 1u)) broken = true;
+      if constexpr (kCodes) copies_wait<kStages - 1>();
       __syncwarp();
+      if (__any_sync(0xffffffffu, broken)) break;
+      filled ^= 1u << st;
       // ---- S^T = K Q^T
       float s[HT][MT][4];
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) s[ht][mt][0] = s[ht][mt][1] = s[ht][mt][2] = s[ht][mt][3] = 0.0f;
+        for (int mt = 0; mt < MT; ++mt) {
+          s[ht][mt][0] = s[ht][mt][2] = s_init[ht][0];
+          s[ht][mt][1] = s[ht][mt][3] = s_init[ht][1];
+        }
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
           uint32_t k0[4], k1[4];  // rows g and g + 8
-          load_piece<16>(k0, stage + ((mt * 2) * KP + i) * 512 + lane * 16);
-          load_piece<16>(k1, stage + ((mt * 2 + 1) * KP + i) * 512 + lane * 16);
+          const uint32_t at = stage + box_offset<Shape, TT>(16 * mt + order, 4 * i + t);
+          load_piece<16>(k0, at);
+          load_piece<16>(k1, at + 8 * Shape::kBox);
           if constexpr (kCodes) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const uint32_t w0 = k0[u] ^ 0x80808080u, w1 = k1[u] ^ 0x80808080u;
-              const uint32_t a0 = codes_f16(w0, 0x4140u), a2 = codes_f16(w0, 0x4342u);
-              const uint32_t a1 = codes_f16(w1, 0x4140u), a3 = codes_f16(w1, 0x4342u);
+              const uint32_t a0 = bytes_f16(w0, 0x4140u), a2 = bytes_f16(w0, 0x4342u);
+              const uint32_t a1 = bytes_f16(w1, 0x4140u), a3 = bytes_f16(w1, 0x4342u);
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht)
                 mma16816<false>(s[ht][mt], a0, a1, a2, a3, qf[ht][4 * i + u][0], qf[ht][4 * i + u][1]);
@@ -430,13 +490,13 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int tok = 16 * mt + 8 * h + g;
+          const int tok = 16 * mt + 8 * h + order;
           const bool hidden = static_cast<uint32_t>(tl) * TT + tok >= count;
           float k_mul = 1.0f;
           vw[mt][h] = 1.0f;
           if constexpr (kCodes) {
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k_mul) : "r"(stage + 2 * Shape::kRowBytes + tok * 4));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vw[mt][h]) : "r"(stage + 2 * Shape::kRowBytes + (TT + tok) * 4));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k_mul) : "r"(scales + st * Shape::kScaleBytes + tok * 4));
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vw[mt][h]) : "r"(scales + st * Shape::kScaleBytes + (TT + tok) * 4));
             move |= vw[mt][h] > v_top;
           }
 #pragma unroll
@@ -484,6 +544,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
               l[ht][c] *= keep;
             }
             keep *= v_keep;
+            o_bias[ht][c] *= keep;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
               o[ht][i][c] *= keep;
@@ -502,7 +563,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float w0 = exp2f(s[ht][mt][2 * h] - z0), w1 = exp2f(s[ht][mt][2 * h + 1] - z1);
+            float w0 = ex2(s[ht][mt][2 * h] - z0), w1 = ex2(s[ht][mt][2 * h + 1] - z1);
             l[ht][0] += w0;
             l[ht][1] += w1;
             if constexpr (kCodes) {
@@ -528,8 +589,11 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         for (int i = 0; i < VP; ++i) {
           uint32_t vr[4][kVBytes / 4];  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            load_piece<kVBytes>(vr[k], stage + Shape::kRowBytes + ((mt * 4 + k) * VP + i) * 32 * kVBytes + lane * kVBytes);
+          for (int k = 0; k < 4; ++k) {
+            const int r = 16 * mt + 8 * (k >> 1) + ((k & 1) ? order_odd : order_even);
+            load_piece<kVBytes>(vr[k], stage + Shape::kRowBytes + (kVBytes == 16 ? box_offset<Shape, TT>(r, 8 * i + g)
+                                                                                : box_offset<Shape, TT>(r, g >> 1) + 8 * (g & 1)));
+          }
 #pragma unroll
           for (int w = 0; w < kVBytes / 4; ++w) {
             const uint32_t va = vr[0][w], vb = vr[1][w], vc = vr[2][w], vd = vr[3][w];
@@ -539,10 +603,10 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
               const uint32_t cd01 = prmt(vc, vd, 0x5140u) ^ 0x80808080u, cd23 = prmt(vc, vd, 0x7362u) ^ 0x80808080u;
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht) {
-                mma16816<false>(o[ht][tile0], codes_f16(ab01, 0x4140u), codes_f16(ab01, 0x4342u),
-                                codes_f16(cd01, 0x4140u), codes_f16(cd01, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
-                mma16816<false>(o[ht][tile0 + 1], codes_f16(ab23, 0x4140u), codes_f16(ab23, 0x4342u),
-                                codes_f16(cd23, 0x4140u), codes_f16(cd23, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
+                mma16816<false>(o[ht][tile0], bytes_f16(ab01, 0x4140u), bytes_f16(ab01, 0x4342u),
+                                bytes_f16(cd01, 0x4140u), bytes_f16(cd01, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
+                mma16816<false>(o[ht][tile0 + 1], bytes_f16(ab23, 0x4140u), bytes_f16(ab23, 0x4342u),
+                                bytes_f16(cd23, 0x4140u), bytes_f16(cd23, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
               }
             } else {  // two channels of two token pairs: one row tile
               const int tile0 = i * (kVBytes / 4) + w;
@@ -558,20 +622,50 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
           }
         }
       }
+      if constexpr (kCodes) {
+        // the bias is a sum of weights that an operand of 128s collects; it leaves O
+        // before it grows large beside it
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            mma16816<false>(o_bias[ht], 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, p[ht][mt][0], p[ht][mt][1]);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            o[ht][i][0] -= o_bias[ht][0];
+            o[ht][i][1] -= o_bias[ht][1];
+            o[ht][i][2] -= o_bias[ht][0];
+            o[ht][i][3] -= o_bias[ht][1];
+          }
+          o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
+        }
+      }
       // ---- refill the stage; its table entries were asked for one tile ago
       __syncwarp();
       if (tl + kStages * kPagedWarps < t1) {
-        issue(stage, row_of(page_next, in_page_next));
-      } else {
+        issue(st, row_of(page_next, in_page_next));
+      } else if constexpr (kCodes) {
         copies_commit();
       }
       page_next = find_page(tl + (kStages + 1) * kPagedWarps, in_page_next);
-      stage = stage + Shape::kStageBytes == ring + Shape::kRing ? ring : stage + Shape::kStageBytes;
+      st = st + 1 == kStages ? 0 : st + 1;
     }
-    copies_wait<0>();
+    if constexpr (kCodes) copies_wait<0>();
+    if (__any_sync(0xffffffffu, broken)) {
+      // copies still on their way are waited for (each wait bounded) before the
+      // shared memory is used for anything else
+      for (int i = 0; i < kStages && tl + i * kPagedWarps < t1; ++i) {
+        const int at = st + i < kStages ? st + i : st + i - kStages;
+        mbar_wait_parity(bars + at, (filled >> at) & 1u);
+        filled ^= 1u << at;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) l[ht][0] = l[ht][1] = NAN;
+    }
 
     // ---- join the warps
-    const float v_undo = 1.0f / v_mul;
+    const float v_undo = (kCodes ? 0x1p24f : 1.0f) / v_mul;
     __syncthreads();  // every warp is done with its ring
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {

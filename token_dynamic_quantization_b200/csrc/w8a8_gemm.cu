@@ -43,6 +43,7 @@
 #include <mutex>
 
 #include "dq.h"
+#include "tensor_map.cuh"
 #include "tma_pipeline.cuh"
 
 namespace {
@@ -649,30 +650,11 @@ __global__ void __launch_bounds__(256) w8a8_gemm_generic_kernel(const W8A8Args a
 
 // ---------------------------------------------------------------- host side
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-    else
-      cudaGetLastError();
-  });
-  return fn;
-}
-
 // [rows, k] int8, k contiguous: 128-byte x box_rows boxes, 128-byte swizzle.
 // Boxes of box_k bytes of K (128: 128-byte swizzle, 64: 64-byte swizzle) by
 // box_rows rows.
 bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, uint32_t box_rows, uint32_t box_k = kBK) {
-  EncodeTiledFn fn = encode_tiled();
+  dq_host::EncodeTiledFn fn = dq_host::encode_tiled();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};  // bytes between rows
