@@ -138,15 +138,15 @@ size_t parts_bytes(int group, int dim) {
   return static_cast<size_t>(most_ctas()) * 2 * (heads * dim + 2 * heads) * sizeof(float);
 }
 
-// A cache as a list of rows, copied four at a time in boxes of 128 bytes (64
-// for 64 codes) with the swizzle of that width.
+// A cache as a list of rows, copied in boxes of 128 bytes (64 for 64 codes) by
+// box_rows with the swizzle of that width (box_rows 1: gathered row by row).
 template <typename C, int BOX>
-bool rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim) {
+bool rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim, int box_rows) {
   dq_host::EncodeTiledFn fn = dq_host::encode_tiled();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(dim) * sizeof(C)};
-  const cuuint32_t box[2] = {static_cast<cuuint32_t>(BOX / sizeof(C)), 1}, estride[2] = {1, 1};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(BOX / sizeof(C)), static_cast<cuuint32_t>(box_rows)}, estride[2] = {1, 1};
   return fn(map, sizeof(C) == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
             const_cast<void*>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
             BOX == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -172,13 +172,14 @@ dq_status launch_pdl(Kernel kernel, dim3 grid, size_t smem, cudaStream_t stream,
   return dq_host::launch_status();
 }
 
-template <typename T, typename C, int D, int HT>
+template <typename T, typename C, int D, int HT, bool RUN>
 dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
   using Shape = dq::PagedShape<C, D, HT>;
-  auto fn = dq::paged_attention_mma_kernel<T, C, D, HT>;
+  auto fn = dq::paged_attention_mma_kernel<T, C, D, HT, RUN>;
   CUtensorMap k_map, v_map;
   const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
-  if (!rows_map<C, Shape::kBox>(&k_map, a.k_cache, rows, D) || !rows_map<C, Shape::kBox>(&v_map, a.v_cache, rows, D))
+  if (!rows_map<C, Shape::kBox>(&k_map, a.k_cache, rows, D, RUN ? 16 : 1) ||
+      !rows_map<C, Shape::kBox>(&v_map, a.v_cache, rows, D, RUN ? 16 : 1))
     return dq_host::kNotLaunchable;
   const int device = dq_host::current_device();
   if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
@@ -197,12 +198,17 @@ dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
                     static_cast<int>(ctas), by_item);
 }
 
+template <typename T, typename C, int D, int HT>
+dq_status by_pages(const dq::PagedArgs& a, cudaStream_t stream) {
+  return a.page_size % 16 == 0 ? launch_mma<T, C, D, HT, true>(a, stream) : launch_mma<T, C, D, HT, false>(a, stream);
+}
+
 template <typename T, typename C>
 dq_status dispatch_mma(const dq::PagedArgs& a, cudaStream_t stream) {
   const int ht = head_tiles(a.group, a.head_dim);
-  if (a.head_dim == 64) return ht == 2 ? launch_mma<T, C, 64, 2>(a, stream) : launch_mma<T, C, 64, 1>(a, stream);
-  if (a.head_dim == 128) return ht == 2 ? launch_mma<T, C, 128, 2>(a, stream) : launch_mma<T, C, 128, 1>(a, stream);
-  return launch_mma<T, C, 256, 1>(a, stream);
+  if (a.head_dim == 64) return ht == 2 ? by_pages<T, C, 64, 2>(a, stream) : by_pages<T, C, 64, 1>(a, stream);
+  if (a.head_dim == 128) return ht == 2 ? by_pages<T, C, 128, 2>(a, stream) : by_pages<T, C, 128, 1>(a, stream);
+  return by_pages<T, C, 256, 1>(a, stream);
 }
 
 template <typename T, typename C>

@@ -109,6 +109,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The value of 16 bits of type T.
+template <typename T>
+__device__ __forceinline__ float half_bits(uint32_t b) {
+  if constexpr (__is_same(T, __nv_bfloat16)) return __uint_as_float(b << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
+}
+
 // Two bytes of w as f16: a byte in the low bits of an f16 is the subnormal byte *
 // 2^-24, exact in the products.
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t w, uint32_t sel) { return prmt(w, 0u, sel); }
@@ -117,6 +131,14 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// A box of a tensor map, from element `x` of row `row` on, to `dst`.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(bar)
+      : "memory");
 }
 
 // Four rows of a tensor map, `x` elements into each, one after the other to
@@ -172,12 +194,48 @@ __device__ __forceinline__ int token_order(int i) {
 
 // ---------------------------------------------------------------- the schedule
 
+// The visible tokens of one sequence as groups of 16 that start at multiples of
+// 16: first those that hold the first tokens [0, first), then those from the
+// one with token `start` on. A length that the page table cannot hold is one
+// token past the table, which makes the rows NaN.
+struct Groups {
+  int len, first, start;
+  int first_groups, count;
+};
+
+__device__ __forceinline__ Groups visible_groups(const PagedArgs& a, int64_t b) {
+  const int64_t room = a.max_pages * a.page_size;
+  const int len = a.lengths[b];
+  Groups v{len, 0, 0, 0, 0};
+  if (len <= 0) {
+    v.len = 0;
+    return v;
+  }
+  if (len > room) {
+    v.start = static_cast<int>(room);
+    v.len = v.start + 1;
+    v.count = 1;
+    return v;
+  }
+  if (a.window != 0 && len > a.window) {
+    v.start = len - static_cast<int>(a.window);
+    v.first = a.sinks < v.start ? static_cast<int>(a.sinks) : v.start;
+    v.first_groups = (v.first + 15) >> 4;
+  }
+  v.count = v.first_groups + (((len - 1) >> 4) - (v.start >> 4) + 1);
+  return v;
+}
+
 // Tiles of one sequence's item; a sequence without tokens still has one, whose
 // CTA writes its zeros.
 template <int TT>
+__device__ __forceinline__ int tiles_of(const Groups& v) {
+  constexpr int kGroups = TT / 16;
+  return v.count == 0 ? 1 : (v.count + kGroups - 1) / kGroups;
+}
+template <int TT>
 __device__ __forceinline__ int64_t item_tiles(const PagedArgs& a, int64_t b) {
-  const int64_t n = (visible_tokens(a, b).count + TT - 1) / TT;
-  return n < 1 ? 1 : n;
+  return tiles_of<TT>(visible_groups(a, b));
 }
 
 __device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
@@ -230,7 +288,7 @@ __device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int64_t ctas) {
 
 // ---------------------------------------------------------------- main kernel
 
-template <typename T, typename C, int D, int HT>
+template <typename T, typename C, int D, int HT, bool RUN>
 __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) paged_attention_mma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                                const PagedArgs a) {
   using Shape = PagedShape<C, D, HT>;
@@ -286,8 +344,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
   const int order_odd = token_order<Shape::kBox>(2 * t + 1);
 
   while (tile < tile_end) {
-    const Visible vis = visible_tokens(a, seq);
-    const int64_t n = vis.count < 1 ? 1 : (vis.count + TT - 1) / TT;
+    const Groups vis = visible_groups(a, seq);
+    const int64_t n = tiles_of<TT>(vis);
     const int64_t item = (tile - base) / n;
     const int64_t item_begin = base + item * n;
     const int t0 = static_cast<int>(tile - item_begin);
@@ -296,67 +354,62 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     const int set = static_cast<int>(item - static_cast<int64_t>(kvh) * a.head_sets);
     const int head0 = kvh * a.group + set * kHeads;                        // first query head
     const int heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
-    const uint32_t count = static_cast<uint32_t>(vis.count), first = static_cast<uint32_t>(vis.first);
     const int32_t* table = a.page_table + seq * a.max_pages;
 
-    // Q as B operands: head g, four channels per k-step
+    // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
+    // per k-step. Beside codes as two signed 8-bit digits, 256 q1 + q0, of a
+    // power of two times it, |.| <= 32639: channels down to 2^-7 (bf16; f16:
+    // 2^-4) of the head's largest are exact, the others within 2^-16 of it.
     uint32_t qf[HT][KS][2];
     float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
-    float s_init[HT][2];  // what the codes' bias of 128 adds to their products, negated
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       const bool on = 8 * ht + g < heads;
       const T* q = static_cast<const T*>(a.q) + seq * a.q_stride + static_cast<int64_t>(head0 + 8 * ht + g) * D;
       float mul = a.softmax_scale * kLog2e;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int c = (s / (kPiece / 4)) * 4 * kPiece + kPiece * t + 4 * (s % (kPiece / 4));
-        uint2 w = make_uint2(0u, 0u);
-        if (on) w = *reinterpret_cast<const uint2*>(q + c);
-        qf[ht][s][0] = w.x;
-        qf[ht][s][1] = w.y;
-      }
-      if constexpr (kCodes && __is_same(T, __nv_bfloat16)) {
-        float top = 0.0f;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ht][s][i] << 16)),
-                                   fabsf(__uint_as_float(qf[ht][s][i] & 0xFFFF0000u))));
-          }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // scaled so that the largest channel lies in [2^14, 2^15): exact down to 2^-28 of it
-        const int e = top > 0.0f && isfinite(top) ? 14 - ilogbf(top) : 0;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            qf[ht][s][i] = pack_f16(scalbnf(__uint_as_float(qf[ht][s][i] << 16), e),
-                                    scalbnf(__uint_as_float(qf[ht][s][i] & 0xFFFF0000u), e));
-          }
-        }
-        mul = scalbnf(mul, -e);
-      }
-      float init = 0.0f;
       if constexpr (kCodes) {
+        uint2 w[KS];  // four channels each
+        uint32_t top = 0u;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&qf[ht][s][i]));
-            init -= f.x + f.y;
-          }
+          w[s] = on ? *reinterpret_cast<const uint2*>(q + (s / 4) * 64 + 16 * t + 4 * (s % 4)) : make_uint2(0u, 0u);
+          top = max(top, max(max(w[s].x & 0x7FFFu, (w[s].x >> 16) & 0x7FFFu), max(w[s].y & 0x7FFFu, (w[s].y >> 16) & 0x7FFFu)));
         }
-        init += __shfl_xor_sync(0xffffffffu, init, 1);
-        init += __shfl_xor_sync(0xffffffffu, init, 2);
-        init *= 0x1p-17f;  // 128 * 2^-24
-        mul *= 0x1p24f;
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float largest = half_bits<T>(top);
+        int e = 0;
+        if (!isfinite(largest)) {
+          mul = NAN;
+        } else if (largest > 0.0f) {
+          e = 14 - ilogbf(largest);
+          if (scalbnf(largest, e) > 32639.0f) --e;
+          if (e > 126) e = 126;
+          mul = scalbnf(mul, -e);
+        }
+        const float f = scalbnf(1.0f, e);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          int x[4] = {__float2int_rn(half_bits<T>(w[s].x & 0xFFFFu) * f), __float2int_rn(half_bits<T>(w[s].x >> 16) * f),
+                      __float2int_rn(half_bits<T>(w[s].y & 0xFFFFu) * f), __float2int_rn(half_bits<T>(w[s].y >> 16) * f)};
+          uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int q1 = (x[i] + 128) >> 8;
+            hi |= (static_cast<uint32_t>(q1) & 255u) << (8 * i);
+            lo |= (static_cast<uint32_t>(x[i] - (q1 << 8)) & 255u) << (8 * i);
+          }
+          qf[ht][s][0] = hi;
+          qf[ht][s][1] = lo;
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 w = on ? *reinterpret_cast<const uint2*>(q + (s / 2) * 32 + 8 * t + 4 * (s % 2)) : make_uint2(0u, 0u);
+          qf[ht][s][0] = w.x;
+          qf[ht][s][1] = w.y;
+        }
       }
-      s_init[ht][0] = __shfl_sync(0xffffffffu, init, 8 * t);
-      s_init[ht][1] = __shfl_sync(0xffffffffu, init, 8 * t + 4);
       q_mul[ht][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
       q_mul[ht][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
     }
@@ -373,12 +426,29 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       for (int i = 0; i < KS; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.0f;
     }
 
-    // lane r finds the cache row of token r of a tile, in two steps so that the
-    // table's latency is off the path: the page, one tile ahead of the row
+    // Token at place r of tile tl, and whether it is visible.
+    const auto token_of = [&](int tl, int r, bool& seen) -> int {
+      const int group = tl * MT + (r >> 4);
+      if (group < vis.first_groups) {
+        const int j = 16 * group + (r & 15);
+        seen = j < vis.first;
+        return j;
+      }
+      const int j = 16 * (group - vis.first_groups) + (vis.start & ~15) + (r & 15);
+      seen = j >= vis.start && j < vis.len;
+      return j;
+    };
+    // Cache row numbers of a tile, in two steps so that the page table's latency
+    // is off the path (the page, one tile ahead of the row): of its groups' first
+    // tokens in lanes 0 .. MT - 1 where pages hold whole groups, else of token r in
+    // lane r. -2: nothing there, -1: no such page.
     const auto find_page = [&](int tl, uint32_t& in_page) -> int32_t {
-      const uint32_t i = static_cast<uint32_t>(tl) * TT + lane;
-      if (tl >= t1 || lane >= TT || i >= count) return -2;
-      const uint32_t j = i < first ? i : i + static_cast<uint32_t>(vis.skip);
+      bool seen;
+      uint32_t j = static_cast<uint32_t>(token_of(tl, RUN ? 16 * lane : lane, seen));
+      if constexpr (RUN) {
+        seen = tl * MT + lane < vis.count && lane < MT;
+      }
+      if (tl >= t1 || !seen || lane >= TT) return -2;
       const uint32_t p = (__umulhi(j, a.page_mul) + j) >> a.page_shift;
       in_page = j - p * static_cast<uint32_t>(a.page_size);
       return p < a.max_pages ? max(__ldg(table + p), -1) : -1;
@@ -393,17 +463,36 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     bool broken = false;  // a page outside the cache, or a copy that never came: the rows become NaN
     const auto issue = [&](int st, uint32_t row) {
       broken |= row == kRowBad;
-      const uint32_t r0 = __shfl_sync(0xffffffffu, row, (4 * lane) & 31), r1 = __shfl_sync(0xffffffffu, row, (4 * lane + 1) & 31);
-      const uint32_t r2 = __shfl_sync(0xffffffffu, row, (4 * lane + 2) & 31), r3 = __shfl_sync(0xffffffffu, row, (4 * lane + 3) & 31);
-      const uint32_t bar = smem_addr(bars + st);
+      const uint32_t bar = smem_addr(bars + st), dst = ring + st * Shape::kStageBytes;
       if (lane == 0) mbar_arrive_expect_tx(bars + st, Shape::kStageBytes);
-      __syncwarp();
-      if (lane < TT / 4) {
-        const uint32_t dst = ring + st * Shape::kStageBytes + lane * 4 * Shape::kBox;
+      if constexpr (RUN) {
+        uint32_t r[MT];
 #pragma unroll
-        for (int x = 0; x < Shape::kBoxes; ++x) {
-          gather_rows(dst + x * TT * Shape::kBox, &k_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
-          gather_rows(dst + Shape::kRowBytes + x * TT * Shape::kBox, &v_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
+        for (int mt = 0; mt < MT; ++mt) r[mt] = __shfl_sync(0xffffffffu, row, mt);
+        if (lane == 0) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int x = 0; x < Shape::kBoxes; ++x) {
+              const uint32_t to = dst + (x * TT + 16 * mt) * Shape::kBox;
+              copy_box(to, &k_map, x * (Shape::kBox / kElem), r[mt], bar);
+              copy_box(to + Shape::kRowBytes, &v_map, x * (Shape::kBox / kElem), r[mt], bar);
+            }
+          }
+        }
+        // from here on lane r's row is token r's
+        const uint32_t mine = lane < 16 ? r[0] : r[MT - 1];
+        row = mine < kRowBad ? mine + (lane & 15) : mine;
+      } else {
+        const uint32_t r0 = __shfl_sync(0xffffffffu, row, (4 * lane) & 31), r1 = __shfl_sync(0xffffffffu, row, (4 * lane + 1) & 31);
+        const uint32_t r2 = __shfl_sync(0xffffffffu, row, (4 * lane + 2) & 31), r3 = __shfl_sync(0xffffffffu, row, (4 * lane + 3) & 31);
+        if (lane < TT / 4) {
+#pragma unroll
+          for (int x = 0; x < Shape::kBoxes; ++x) {
+            const uint32_t to = dst + (x * TT + 4 * lane) * Shape::kBox;
+            gather_rows(to, &k_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
+            gather_rows(to + Shape::kRowBytes, &v_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
+          }
         }
       }
       if constexpr (kCodes) {
@@ -446,33 +535,48 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       filled ^= 1u << st;
       // ---- S^T = K Q^T
       float s[HT][MT][4];
-#pragma unroll
-      for (int ht = 0; ht < HT; ++ht) {
+      if constexpr (kCodes) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          s[ht][mt][0] = s[ht][mt][2] = s_init[ht][0];
-          s[ht][mt][1] = s[ht][mt][3] = s_init[ht][1];
-        }
-      }
+          uint32_t k0[KP][4], k1[KP][4];  // rows g and g + 8
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+          for (int i = 0; i < KP; ++i) {
+            const uint32_t at = stage + box_offset<Shape, TT>(16 * mt + order, 4 * i + t);
+            load_piece<16>(k0[i], at);
+            load_piece<16>(k1[i], at + 8 * Shape::kBox);
+          }
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-          uint32_t k0[4], k1[4];  // rows g and g + 8
-          const uint32_t at = stage + box_offset<Shape, TT>(16 * mt + order, 4 * i + t);
-          load_piece<16>(k0, at);
-          load_piece<16>(k1, at + 8 * Shape::kBox);
-          if constexpr (kCodes) {
+          for (int ht = 0; ht < HT; ++ht) {
+            int d[4] = {0, 0, 0, 0};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint32_t w0 = k0[u] ^ 0x80808080u, w1 = k1[u] ^ 0x80808080u;
-              const uint32_t a0 = bytes_f16(w0, 0x4140u), a2 = bytes_f16(w0, 0x4342u);
-              const uint32_t a1 = bytes_f16(w1, 0x4140u), a3 = bytes_f16(w1, 0x4342u);
+            for (int digit = 0; digit < 2; ++digit) {
+              if (digit == 1) d[0] <<= 8, d[1] <<= 8, d[2] <<= 8, d[3] <<= 8;
 #pragma unroll
-              for (int ht = 0; ht < HT; ++ht)
-                mma16816<false>(s[ht][mt], a0, a1, a2, a3, qf[ht][4 * i + u][0], qf[ht][4 * i + u][1]);
+              for (int i = 0; i < KP; ++i) {
+#pragma unroll
+                for (int u = 0; u < 4; u += 2)
+                  mma16832_s8(d, k0[i][u], k1[i][u], k0[i][u + 1], k1[i][u + 1], qf[ht][4 * i + u][digit],
+                              qf[ht][4 * i + u + 1][digit]);
+              }
             }
-          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) s[ht][mt][x] = __int2float_rn(d[x]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) s[ht][mt][0] = s[ht][mt][1] = s[ht][mt][2] = s[ht][mt][3] = 0.0f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+          for (int i = 0; i < KP; ++i) {
+            uint32_t k0[4], k1[4];  // rows g and g + 8
+            const uint32_t at = stage + box_offset<Shape, TT>(16 * mt + order, 4 * i + t);
+            load_piece<16>(k0, at);
+            load_piece<16>(k1, at + 8 * Shape::kBox);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -485,18 +589,21 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       }
       // ---- scores in log2, hidden tokens out
       float vw[MT][2];
-      bool move = false;
+      bool move = false, edge = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int tok = 16 * mt + 8 * h + order;
-          const bool hidden = static_cast<uint32_t>(tl) * TT + tok >= count;
+          bool seen;
+          token_of(tl, tok, seen);
+          edge |= !seen;
           float k_mul = 1.0f;
           vw[mt][h] = 1.0f;
           if constexpr (kCodes) {
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k_mul) : "r"(scales + st * Shape::kScaleBytes + tok * 4));
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vw[mt][h]) : "r"(scales + st * Shape::kScaleBytes + (TT + tok) * 4));
+            if (!seen) vw[mt][h] = 0.0f;
             move |= vw[mt][h] > v_top;
           }
 #pragma unroll
@@ -505,10 +612,29 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
             for (int c = 0; c < 2; ++c) {
               float& x = s[ht][mt][2 * h + c];
               x *= kCodes ? k_mul * q_mul[ht][c] : q_mul[ht][c];
-              if (hidden) x = -INFINITY;
+              if (!seen) x = -INFINITY;
               move |= x > m[ht][c] + kSlack;
             }
           }
+        }
+      }
+      // hidden tokens of a group that was copied whole may hold anything: their
+      // values have to be finite beside weights of zero (codes always are)
+      if constexpr (RUN && !kCodes) {
+        if (__any_sync(0xffffffffu, edge)) {
+          bool seen;
+          token_of(tl, lane, seen);
+          if (lane < TT && !seen) {
+#pragma unroll
+            for (int x = 0; x < Shape::kBoxes; ++x) {
+#pragma unroll
+              for (int i = 0; i < Shape::kBox; i += 16)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(stage + Shape::kRowBytes + (x * TT + lane) * Shape::kBox + i), "r"(0u)
+                             : "memory");
+            }
+          }
+          fence_proxy_async_smem();  // before the next copy into these rows
+          __syncwarp();
         }
       }
       // ---- the running maximum and the largest value scale, when they have to move
@@ -713,7 +839,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       }
       if (complete) {
         const int64_t at = seq * a.q_heads + head0 + h;
-        const float r = vis.count == 0 ? 0.0f : 1.0f / total;
+        const float r = vis.len == 0 ? 0.0f : 1.0f / total;
         T* out = static_cast<T*>(a.out) + at * D + c;
         uint2 w;
         if constexpr (__is_same(T, __nv_bfloat16)) {
@@ -723,7 +849,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         }
         *reinterpret_cast<uint2*>(out) = w;
         if (a.lse != nullptr && c == 0)
-          a.lse[at] = vis.count == 0 ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
+          a.lse[at] = vis.len == 0 ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(part + h * D + c) = sum;
         if (c == 0) {
