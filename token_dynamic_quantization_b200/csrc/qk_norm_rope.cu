@@ -42,6 +42,8 @@ struct NormRopeArgs {
   const int64_t* slots;
   int64_t num_slots;
   int page_size;
+  int parts;       // vector kernel: warps that share a token's rows
+  int lane_shift;  // vector kernel: log2 of the lanes per row
 };
 
 enum : int { kCacheNone = 0, kCacheSame = 1, kCacheInt8 = 2 };
@@ -193,6 +195,235 @@ __global__ void __launch_bounds__(kNormRopeBlock) norm_rope_generic_kernel(const
   }
 }
 
+// ---- vector kernel
+
+// VEC values of one chunk (8: 16 bytes, 4: 8 bytes).
+template <typename T, int VEC>
+struct Chunk {
+  uint32_t w[VEC / 2];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 8) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (VEC == 8) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void widen(float (&f)[VEC]) const {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void narrow(const float (&f)[VEC]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      if constexpr (__is_same(T, __nv_bfloat16)) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_weights(const void* p, int dtype, int c, float (&w)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) w[i] = p == nullptr ? 1.0f : load_param(p, dtype, c + i);
+}
+
+// A warp takes one token and loops over its head rows, 32 / L rows at a time,
+// L the power of two that covers head_dim / (2 VEC) lanes: each lane holds two
+// chunks of VEC channels, those that rotate with each other (i and i +
+// rope_dim / 2) or two neighbouring ones (interleaved pairs, channels past
+// rope_dim), so the rotation needs no exchange and its VEC angles are computed
+// once per token and lane, not once per row. The next rows are loaded before the
+// current ones are worked on. Few tokens: `parts` warps share one token's rows.
+template <typename T, int VEC, int CACHE>
+__global__ void __launch_bounds__(kNormRopeBlock, 2) norm_rope_kernel(const NormRopeArgs a) {
+  pdl_launch_dependents();
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31;
+  const int64_t work = static_cast<int64_t>(blockIdx.x) * (kNormRopeBlock / 32) + (threadIdx.x >> 5);
+  const int64_t token = work / a.parts;
+  if (token >= a.tokens) return;
+  const int part = static_cast<int>(work - token * a.parts);
+  const int rows_at_once = 32 >> a.lane_shift, l = lane & ((1 << a.lane_shift) - 1);
+  const int heads = a.q_heads + a.kv_heads * (CACHE == kCacheNone ? 1 : 2);
+
+  // the lane's chunks and their angles
+  const int half = a.rope_dim / 2, pair_chunks = a.interleaved ? 0 : half / VEC;
+  const bool split = l < pair_chunks;
+  const int c0 = (split ? l : pair_chunks + 2 * (l - pair_chunks) + pair_chunks) * VEC;
+  const int c1 = split ? c0 + half : c0 + VEC;
+  const bool in = c1 < a.head_dim;
+  const bool turn0 = in && (split || (a.interleaved && c0 < a.rope_dim)), turn1 = in && a.interleaved && c1 < a.rope_dim;
+  float cs[VEC], sn[VEC];
+  {
+    const int32_t pos = a.positions[token];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      // split: angle c0 + i; interleaved: angles c0 / 2 .. of the first chunk, then c1 / 2 .. of the second
+      const int k = split ? c0 + i : (i < VEC / 2 ? c0 / 2 + i : c1 / 2 + i - VEC / 2);
+      cs[i] = 1.0f;
+      sn[i] = 0.0f;
+      if (i < VEC / 2 || split ? turn0 : turn1) rope_angle(pos, a.inv_freq[k], cs[i], sn[i]);
+    }
+  }
+  int64_t slot = -1, page = 0;
+  if (CACHE != kCacheNone) {
+    slot = a.slots[token];
+    if (slot >= a.num_slots) slot = -1;
+    if (slot >= 0) page = slot / a.page_size;
+  }
+  const T* q = static_cast<const T*>(a.q) + token * a.q_stride;
+  const T* k = static_cast<const T*>(a.k) + token * a.k_stride;
+  const T* v = static_cast<const T*>(a.v) + (CACHE == kCacheNone ? 0 : token * a.v_stride);
+
+  // row `h` of the token: 0 query, 1 key, 2 value, and its number there
+  const auto locate = [&](int h, int& which, int& at) -> const T* {
+    which = h < a.q_heads ? 0 : (h < a.q_heads + a.kv_heads ? 1 : 2);
+    at = h - (which == 0 ? 0 : (which == 1 ? a.q_heads : a.q_heads + a.kv_heads));
+    return (which == 0 ? q : (which == 1 ? k : v)) + static_cast<int64_t>(at) * a.head_dim;
+  };
+  const int step = rows_at_once * a.parts;
+  int h = part * rows_at_once + (lane >> a.lane_shift);
+  int which, at, loaded = -1;
+  float w0[VEC], w1[VEC];
+  Chunk<T, VEC> x0, x1;
+  const auto fetch = [&](int row) {
+    x0.clear();
+    x1.clear();
+    if (row < heads && in) {
+      const T* p = locate(row, which, at);
+      x0.load(p + c0);
+      x1.load(p + c1);
+    }
+  };
+  fetch(h);
+  // the bound is the same for the whole warp: its lanes meet in the reductions
+  for (int first = part * rows_at_once; first < heads; first += step, h += step) {
+    float f0[VEC], f1[VEC];
+    x0.widen(f0);
+    x1.widen(f1);
+    const bool live = h < heads;
+    locate(live ? h : 0, which, at);
+    const int row_which = which, row_at = at;
+    fetch(h + step);
+    const bool normed = row_which != 2;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], sum));
+    for (int o = 1; o < (1 << a.lane_shift); o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (normed) {
+      if (loaded != row_which && in) {  // at the first row, and where the queries end
+        loaded = row_which;
+        load_weights<VEC>(row_which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c0, w0);
+        load_weights<VEC>(row_which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c1, w1);
+      }
+      const float r = rsqrtf(fmaf(sum, a.inv_dim, a.epsilon));
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        f0[i] = f0[i] * r * w0[i];
+        f1[i] = f1[i] * r * w1[i];
+      }
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+          const float y0 = f0[i], y1 = f0[i + 1], z0 = f1[i], z1 = f1[i + 1];
+          f0[i] = y0 * cs[i / 2] - y1 * sn[i / 2];
+          f0[i + 1] = y1 * cs[i / 2] + y0 * sn[i / 2];
+          f1[i] = z0 * cs[VEC / 2 + i / 2] - z1 * sn[VEC / 2 + i / 2];
+          f1[i + 1] = z1 * cs[VEC / 2 + i / 2] + z0 * sn[VEC / 2 + i / 2];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float y0 = f0[i], y1 = f1[i];
+          f0[i] = y0 * cs[i] - y1 * sn[i];
+          f1[i] = y1 * cs[i] + y0 * sn[i];
+        }
+      }
+    }
+    int64_t cache_row = 0;
+    if (CACHE != kCacheNone) cache_row = (page * a.kv_heads + row_at) * a.page_size + (slot - page * a.page_size);
+    if constexpr (CACHE == kCacheInt8) {
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) top = fmaxf(top, fmaxf(fabsf(f0[i]), fabsf(f1[i])));
+      for (int o = 1; o < (1 << a.lane_shift); o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (row_which != 0) {
+        if (live && slot >= 0) {
+          const RowQuant rq = make_sym<127>(top);
+          uint32_t bits[8];
+          int8_t* y = static_cast<int8_t*>(row_which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
+          const auto codes = [&](const float(&f)[8]) -> uint2 {
+            if (rq.zero_scale) return make_uint2(0u, 0u);
+            if (rq.exact_row) {
+              quant8_exact<false>(f, rq, -127.0f, 127.0f, bits);
+            } else {
+              quant8<false, false>(f, rq, -127.0f, 127.0f, bits);
+            }
+            return pack8_int8(bits);
+          };
+          if constexpr (VEC == 8) {
+            const uint2 b0 = codes(f0), b1 = codes(f1);
+            if (in) {
+              *reinterpret_cast<uint2*>(y + c0) = b0;
+              *reinterpret_cast<uint2*>(y + c1) = b1;
+            }
+          } else {
+            const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
+            const uint2 b = codes(f);
+            if (in) {
+              *reinterpret_cast<uint32_t*>(y + c0) = b.x;
+              *reinterpret_cast<uint32_t*>(y + c1) = b.y;
+            }
+          }
+          if (l == 0) (row_which == 1 ? a.k_scale : a.v_scale)[cache_row] = rq.scale;
+        }
+        continue;
+      }
+    }
+    if (!live || !in || (CACHE != kCacheNone && row_which != 0 && slot < 0)) continue;
+    T* y;
+    if (row_which == 0) {
+      y = static_cast<T*>(a.q_out) + token * a.q_out_stride + static_cast<int64_t>(row_at) * a.head_dim;
+    } else if (CACHE == kCacheNone) {
+      y = static_cast<T*>(a.k_out) + token * a.k_out_stride + static_cast<int64_t>(row_at) * a.head_dim;
+    } else {
+      y = static_cast<T*>(row_which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
+    }
+    Chunk<T, VEC> o0, o1;
+    o0.narrow(f0);
+    o1.narrow(f1);
+    o0.store(y + c0);
+    o1.store(y + c1);
+  }
+}
+
 }  // namespace dq
 
 namespace {
@@ -210,11 +441,47 @@ dq_status launch_generic(const dq::NormRopeArgs& a, cudaStream_t stream) {
                                       stream);
 }
 
+// Whether every row splits into aligned chunks of `vec` values, two to a lane:
+// pairs (i, i + rope_dim / 2) lie in two chunks, the rest in pairs of chunks.
+bool vector_ok(const dq::NormRopeArgs& a, int cache, int vec) {
+  const int bytes = 2 * vec, codes = vec;
+  if (a.head_dim % (2 * vec) != 0) return false;
+  if (a.interleaved ? a.rope_dim % vec != 0 : a.rope_dim / 2 % vec != 0) return false;
+  const auto rows = [&](const void* p, int64_t stride) { return aligned(p, bytes) && stride % vec == 0; };
+  if (!rows(a.q, a.q_stride) || !rows(a.k, a.k_stride) || !rows(a.q_out, a.q_out_stride)) return false;
+  if (cache == dq::kCacheNone) return rows(a.k_out, a.k_out_stride);
+  const int at = cache == dq::kCacheInt8 ? codes : bytes;
+  return rows(a.v, a.v_stride) && aligned(a.k_cache, at) && aligned(a.v_cache, at);
+}
+
+template <typename T, int VEC, int CACHE>
+dq_status launch_vector(dq::NormRopeArgs a, cudaStream_t stream) {
+  void (*fn)(const dq::NormRopeArgs) = dq::norm_rope_kernel<T, VEC, CACHE>;
+  const int heads = a.q_heads + a.kv_heads * (CACHE == dq::kCacheNone ? 1 : 2);
+  a.lane_shift = 0;
+  while ((1 << a.lane_shift) * 2 * VEC < a.head_dim) ++a.lane_shift;
+  // warps per token: one row each while the warps leave the device empty
+  const int groups = (heads + (32 >> a.lane_shift) - 1) / (32 >> a.lane_shift);
+  const int64_t room = static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * 16;
+  int64_t parts = room / a.tokens;
+  a.parts = static_cast<int>(parts < 1 ? 1 : (parts > groups ? groups : parts));
+  const int64_t warps = a.tokens * a.parts;
+  const int64_t grid = (warps + dq::kNormRopeBlock / 32 - 1) / (dq::kNormRopeBlock / 32);
+  return dq_host::launch_programmatic(fn, a, static_cast<int>(grid), dq::kNormRopeBlock, 0, stream);
+}
+
+template <typename T, int CACHE>
+dq_status launch(const dq::NormRopeArgs& a, cudaStream_t stream) {
+  if (vector_ok(a, CACHE, 8)) return launch_vector<T, 8, CACHE>(a, stream);
+  if (vector_ok(a, CACHE, 4)) return launch_vector<T, 4, CACHE>(a, stream);
+  return launch_generic<T, CACHE>(a, stream);
+}
+
 template <typename T>
 dq_status dispatch(const dq::NormRopeArgs& a, int cache, cudaStream_t stream) {
-  if (cache == dq::kCacheNone) return launch_generic<T, dq::kCacheNone>(a, stream);
-  if (cache == dq::kCacheSame) return launch_generic<T, dq::kCacheSame>(a, stream);
-  return launch_generic<T, dq::kCacheInt8>(a, stream);
+  if (cache == dq::kCacheNone) return launch<T, dq::kCacheNone>(a, stream);
+  if (cache == dq::kCacheSame) return launch<T, dq::kCacheSame>(a, stream);
+  return launch<T, dq::kCacheInt8>(a, stream);
 }
 
 bool is_param_float(dq_dtype t) { return t == DQ_F32 || t == DQ_F16 || t == DQ_BF16; }
