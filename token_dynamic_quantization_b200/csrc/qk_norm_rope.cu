@@ -72,7 +72,14 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) {
   return __float2bfloat16_rn(v);
 }
 
-constexpr int kNormRopeBlock = 256;
+constexpr int kNormRopeBlock = 128;
+#ifndef DQ_NR_CTAS
+#define DQ_NR_CTAS 4
+#endif
+#ifndef DQ_NR_DEPTH
+#define DQ_NR_DEPTH 2
+#endif
+constexpr int kDepth = DQ_NR_DEPTH;
 
 // Any head dimension, stride and alignment: one warp per (token, head row),
 // the row in registers (rotation pairs lane, lane + 32, ..., then the channels
@@ -221,27 +228,24 @@ struct Chunk {
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) w[i] = 0u;
   }
-  __device__ __forceinline__ void widen(float (&f)[VEC]) const {
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i) {
-      if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      } else {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-      }
-    }
-  }
-  __device__ __forceinline__ void narrow(const float (&f)[VEC]) {
+  __device__ __forceinline__ void widen(float2 (&f)[VEC / 2]) const {
 #pragma unroll
     for (int i = 0; i < VEC / 2; ++i) {
       if constexpr (__is_same(T, __nv_bfloat16)) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+      } else {
+        f[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      }
+    }
+  }
+  __device__ __forceinline__ void narrow(const float2 (&f)[VEC / 2]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+      if constexpr (__is_same(T, __nv_bfloat16)) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[i].x, f[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       } else {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        const __half2 h = __floats2half2_rn(f[i].x, f[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
@@ -249,20 +253,23 @@ struct Chunk {
 };
 
 template <int VEC>
-__device__ __forceinline__ void load_weights(const void* p, int dtype, int c, float (&w)[VEC]) {
+__device__ __forceinline__ void load_weights(const void* p, int dtype, int c, float2 (&w)[VEC / 2]) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) w[i] = p == nullptr ? 1.0f : load_param(p, dtype, c + i);
+  for (int i = 0; i < VEC / 2; ++i)
+    w[i] = p == nullptr ? make_float2(1.0f, 1.0f)
+                        : make_float2(load_param(p, dtype, c + 2 * i), load_param(p, dtype, c + 2 * i + 1));
 }
 
 // A warp takes one token and loops over its head rows, 32 / L rows at a time,
 // L the power of two that covers head_dim / (2 VEC) lanes: each lane holds two
 // chunks of VEC channels, those that rotate with each other (i and i +
 // rope_dim / 2) or two neighbouring ones (interleaved pairs, channels past
-// rope_dim), so the rotation needs no exchange and its VEC angles are computed
-// once per token and lane, not once per row. The next rows are loaded before the
-// current ones are worked on. Few tokens: `parts` warps share one token's rows.
+// rope_dim), so the rotation needs no exchange. A token's angles are computed
+// once, each by one lane, and handed round. kDepth sets of rows are in flight
+// while one is worked on. Few tokens: `parts` warps share one token's rows.
 template <typename T, int VEC, int CACHE>
-__global__ void __launch_bounds__(kNormRopeBlock, 2) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int H = VEC / 2;
   pdl_launch_dependents();
   pdl_wait_primary();
   const int lane = threadIdx.x & 31;
@@ -270,157 +277,200 @@ __global__ void __launch_bounds__(kNormRopeBlock, 2) norm_rope_kernel(const Norm
   const int64_t token = work / a.parts;
   if (token >= a.tokens) return;
   const int part = static_cast<int>(work - token * a.parts);
-  const int rows_at_once = 32 >> a.lane_shift, l = lane & ((1 << a.lane_shift) - 1);
+  const int lanes = 1 << a.lane_shift, rows_at_once = 32 >> a.lane_shift, l = lane & (lanes - 1);
   const int heads = a.q_heads + a.kv_heads * (CACHE == kCacheNone ? 1 : 2);
 
-  // the lane's chunks and their angles
+  // the lane's chunks
   const int half = a.rope_dim / 2, pair_chunks = a.interleaved ? 0 : half / VEC;
   const bool split = l < pair_chunks;
   const int c0 = (split ? l : pair_chunks + 2 * (l - pair_chunks) + pair_chunks) * VEC;
   const int c1 = split ? c0 + half : c0 + VEC;
   const bool in = c1 < a.head_dim;
-  const bool turn0 = in && (split || (a.interleaved && c0 < a.rope_dim)), turn1 = in && a.interleaved && c1 < a.rope_dim;
-  float cs[VEC], sn[VEC];
-  {
+
+  const T* q = static_cast<const T*>(a.q) + token * a.q_stride + c0;
+  const T* k = static_cast<const T*>(a.k) + token * a.k_stride + c0;
+  const T* v = static_cast<const T*>(a.v) + (CACHE == kCacheNone ? 0 : token * a.v_stride) + c0;
+  const int apart = c1 - c0;
+  // row `h` of the token: 0 query, 1 key, 2 value, and its number there
+  const auto kind = [&](int h) -> int { return h < a.q_heads ? 0 : (h < a.q_heads + a.kv_heads ? 1 : 2); };
+  const auto number = [&](int h, int which) -> int {
+    return h - (which == 0 ? 0 : (which == 1 ? a.q_heads : a.q_heads + a.kv_heads));
+  };
+  const int step = rows_at_once * a.parts;
+  const int begin = part * rows_at_once;
+  int h = begin + (lane >> a.lane_shift);
+  Chunk<T, VEC> x0[kDepth], x1[kDepth];
+  const auto fetch = [&](int row, Chunk<T, VEC>& y0, Chunk<T, VEC>& y1) {
+    if (row < heads && in) {
+      const int which = kind(row);
+      const T* p = (which == 0 ? q : (which == 1 ? k : v)) + number(row, which) * a.head_dim;
+      y0.load(p);
+      y1.load(p + apart);
+    } else {
+      y0.clear();
+      y1.clear();
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d) fetch(h + d * step, x0[d], x1[d]);
+
+  // Angles: angle i turns channels (i, i + rope_dim / 2), or (2i, 2i + 1). Lane j
+  // computes angles j, j + 32, ... and every lane picks its own VEC.
+  float2 cs[H], sn[H];
+#pragma unroll
+  for (int i = 0; i < H; ++i) {
+    cs[i] = make_float2(1.0f, 1.0f);
+    sn[i] = make_float2(0.0f, 0.0f);
+  }
+  if (half > 0) {
     const int32_t pos = a.positions[token];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      // split: angle c0 + i; interleaved: angles c0 / 2 .. of the first chunk, then c1 / 2 .. of the second
-      const int k = split ? c0 + i : (i < VEC / 2 ? c0 / 2 + i : c1 / 2 + i - VEC / 2);
-      cs[i] = 1.0f;
-      sn[i] = 0.0f;
-      if (i < VEC / 2 || split ? turn0 : turn1) rope_angle(pos, a.inv_freq[k], cs[i], sn[i]);
+    for (int set = 0; set < DQ_MAX_HEAD_DIM / 64; ++set) {
+      if (32 * set < half) {
+        float c = 1.0f, s = 0.0f;
+        if (32 * set + lane < half) rope_angle(pos, a.inv_freq[32 * set + lane], c, s);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          // split: c0 + i; interleaved: c0 / 2 ... of the first chunk, then c1 / 2 ... of the second
+          const int want = a.interleaved ? (i < H ? c0 / 2 + i : c1 / 2 + i - H) : c0 + i;
+          const float cw = __shfl_sync(0xffffffffu, c, want & 31), sw = __shfl_sync(0xffffffffu, s, want & 31);
+          const bool mine = (want >> 5) == set && want < half && (a.interleaved || split);
+          float& cd = i & 1 ? cs[i / 2].y : cs[i / 2].x;
+          float& sd = i & 1 ? sn[i / 2].y : sn[i / 2].x;
+          if (mine) {
+            cd = cw;
+            sd = sw;
+          }
+        }
+      }
     }
   }
-  int64_t slot = -1, page = 0;
+  int64_t slot = -1, page_row = 0;
   if (CACHE != kCacheNone) {
     slot = a.slots[token];
     if (slot >= a.num_slots) slot = -1;
-    if (slot >= 0) page = slot / a.page_size;
+    if (slot >= 0) {
+      const int64_t page = slot / a.page_size;
+      page_row = page * a.kv_heads * a.page_size + (slot - page * a.page_size);
+    }
   }
-  const T* q = static_cast<const T*>(a.q) + token * a.q_stride;
-  const T* k = static_cast<const T*>(a.k) + token * a.k_stride;
-  const T* v = static_cast<const T*>(a.v) + (CACHE == kCacheNone ? 0 : token * a.v_stride);
+  int loaded = -1;
+  float2 w0[H], w1[H];
 
-  // row `h` of the token: 0 query, 1 key, 2 value, and its number there
-  const auto locate = [&](int h, int& which, int& at) -> const T* {
-    which = h < a.q_heads ? 0 : (h < a.q_heads + a.kv_heads ? 1 : 2);
-    at = h - (which == 0 ? 0 : (which == 1 ? a.q_heads : a.q_heads + a.kv_heads));
-    return (which == 0 ? q : (which == 1 ? k : v)) + static_cast<int64_t>(at) * a.head_dim;
-  };
-  const int step = rows_at_once * a.parts;
-  int h = part * rows_at_once + (lane >> a.lane_shift);
-  int which, at, loaded = -1;
-  float w0[VEC], w1[VEC];
-  Chunk<T, VEC> x0, x1;
-  const auto fetch = [&](int row) {
-    x0.clear();
-    x1.clear();
-    if (row < heads && in) {
-      const T* p = locate(row, which, at);
-      x0.load(p + c0);
-      x1.load(p + c1);
-    }
-  };
-  fetch(h);
-  // the bound is the same for the whole warp: its lanes meet in the reductions
-  for (int first = part * rows_at_once; first < heads; first += step, h += step) {
-    float f0[VEC], f1[VEC];
-    x0.widen(f0);
-    x1.widen(f1);
-    const bool live = h < heads;
-    locate(live ? h : 0, which, at);
-    const int row_which = which, row_at = at;
-    fetch(h + step);
-    const bool normed = row_which != 2;
-    float sum = 0.0f;
+  const auto work_on = [&](int first, int row, const Chunk<T, VEC>& r0, const Chunk<T, VEC>& r1) {
+    float2 f0[H], f1[H];
+    r0.widen(f0);
+    r1.widen(f1);
+    const bool live = row < heads;
+    const int which = live ? kind(row) : (CACHE == kCacheNone ? 1 : 2), at = number(row, which);
+    float r = 1.0f;
+    if (first < a.q_heads + a.kv_heads) {  // some row of the warp is normed
+      float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sum = fmaf(f0[i], f0[i], fmaf(f1[i], f1[i], sum));
-    for (int o = 1; o < (1 << a.lane_shift); o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (normed) {
-      if (loaded != row_which && in) {  // at the first row, and where the queries end
-        loaded = row_which;
-        load_weights<VEC>(row_which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c0, w0);
-        load_weights<VEC>(row_which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c1, w1);
+      for (int i = 0; i < H; ++i) sum2 = __ffma2_rn(f0[i], f0[i], __ffma2_rn(f1[i], f1[i], sum2));
+      float sum = sum2.x + sum2.y;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
-      const float r = rsqrtf(fmaf(sum, a.inv_dim, a.epsilon));
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        f0[i] = f0[i] * r * w0[i];
-        f1[i] = f1[i] * r * w1[i];
-      }
-      if (a.interleaved) {
-#pragma unroll
-        for (int i = 0; i < VEC; i += 2) {
-          const float y0 = f0[i], y1 = f0[i + 1], z0 = f1[i], z1 = f1[i + 1];
-          f0[i] = y0 * cs[i / 2] - y1 * sn[i / 2];
-          f0[i + 1] = y1 * cs[i / 2] + y0 * sn[i / 2];
-          f1[i] = z0 * cs[VEC / 2 + i / 2] - z1 * sn[VEC / 2 + i / 2];
-          f1[i + 1] = z1 * cs[VEC / 2 + i / 2] + z0 * sn[VEC / 2 + i / 2];
+      if (which != 2) {
+        if (loaded != which && in) {  // at the first row, and where the queries end
+          loaded = which;
+          load_weights<VEC>(which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c0, w0);
+          load_weights<VEC>(which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c1, w1);
         }
-      } else {
+        r = rsqrtf(fmaf(sum, a.inv_dim, a.epsilon));
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float y0 = f0[i], y1 = f1[i];
-          f0[i] = y0 * cs[i] - y1 * sn[i];
-          f1[i] = y1 * cs[i] + y0 * sn[i];
+        for (int i = 0; i < H; ++i) {
+          f0[i] = __fmul2_rn(__fmul2_rn(f0[i], f2(r)), w0[i]);
+          f1[i] = __fmul2_rn(__fmul2_rn(f1[i], f2(r)), w1[i]);
+        }
+        if (a.interleaved) {
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            const float ca = i & 1 ? cs[i / 2].y : cs[i / 2].x, sa = i & 1 ? sn[i / 2].y : sn[i / 2].x;
+            const float cb = i & 1 ? cs[(H + i) / 2].y : cs[(H + i) / 2].x, sb = i & 1 ? sn[(H + i) / 2].y : sn[(H + i) / 2].x;
+            f0[i] = make_float2(f0[i].x * ca - f0[i].y * sa, f0[i].y * ca + f0[i].x * sa);
+            f1[i] = make_float2(f1[i].x * cb - f1[i].y * sb, f1[i].y * cb + f1[i].x * sb);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            const float2 y0 = f0[i], y1 = f1[i];
+            f0[i] = __ffma2_rn(y0, cs[i], __fmul2_rn(y1, make_float2(-sn[i].x, -sn[i].y)));
+            f1[i] = __ffma2_rn(y1, cs[i], __fmul2_rn(y0, sn[i]));
+          }
         }
       }
     }
-    int64_t cache_row = 0;
-    if (CACHE != kCacheNone) cache_row = (page * a.kv_heads + row_at) * a.page_size + (slot - page * a.page_size);
+    const int64_t cache_row = page_row + static_cast<int64_t>(at) * a.page_size;
     if constexpr (CACHE == kCacheInt8) {
-      float top = 0.0f;
+      if (first + rows_at_once > a.q_heads) {  // some row of the warp becomes codes
+        float top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) top = fmaxf(top, fmaxf(fabsf(f0[i]), fabsf(f1[i])));
-      for (int o = 1; o < (1 << a.lane_shift); o *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (row_which != 0) {
-        if (live && slot >= 0) {
-          const RowQuant rq = make_sym<127>(top);
-          uint32_t bits[8];
-          int8_t* y = static_cast<int8_t*>(row_which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
-          const auto codes = [&](const float(&f)[8]) -> uint2 {
-            if (rq.zero_scale) return make_uint2(0u, 0u);
-            if (rq.exact_row) {
-              quant8_exact<false>(f, rq, -127.0f, 127.0f, bits);
+        for (int i = 0; i < H; ++i)
+          top = max3(top, fmaxf(fabsf(f0[i].x), fabsf(f0[i].y)), fmaxf(fabsf(f1[i].x), fabsf(f1[i].y)));
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+          if (o < lanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        }
+        if (which != 0) {
+          if (live && slot >= 0 && in) {
+            RowQuant rq = make_sym<127>(top);
+            int8_t* y = static_cast<int8_t*>(which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
+            uint32_t bits[8];
+            const auto codes = [&](const float(&f)[8]) -> uint2 {
+              if (rq.zero_scale) return make_uint2(0u, 0u);
+              if (rq.exact_row) {
+                quant8_exact<false>(f, rq, -127.0f, 127.0f, bits);
+              } else {
+                quant8<false, false>(f, rq, -127.0f, 127.0f, bits);
+              }
+              return pack8_int8(bits);
+            };
+            if constexpr (VEC == 8) {
+              const float a0[8] = {f0[0].x, f0[0].y, f0[1].x, f0[1].y, f0[2].x, f0[2].y, f0[3].x, f0[3].y};
+              const float a1[8] = {f1[0].x, f1[0].y, f1[1].x, f1[1].y, f1[2].x, f1[2].y, f1[3].x, f1[3].y};
+              *reinterpret_cast<uint2*>(y + c0) = codes(a0);
+              *reinterpret_cast<uint2*>(y + c1) = codes(a1);
             } else {
-              quant8<false, false>(f, rq, -127.0f, 127.0f, bits);
-            }
-            return pack8_int8(bits);
-          };
-          if constexpr (VEC == 8) {
-            const uint2 b0 = codes(f0), b1 = codes(f1);
-            if (in) {
-              *reinterpret_cast<uint2*>(y + c0) = b0;
-              *reinterpret_cast<uint2*>(y + c1) = b1;
-            }
-          } else {
-            const float f[8] = {f0[0], f0[1], f0[2], f0[3], f1[0], f1[1], f1[2], f1[3]};
-            const uint2 b = codes(f);
-            if (in) {
+              const float f[8] = {f0[0].x, f0[0].y, f0[1].x, f0[1].y, f1[0].x, f1[0].y, f1[1].x, f1[1].y};
+              const uint2 b = codes(f);
               *reinterpret_cast<uint32_t*>(y + c0) = b.x;
               *reinterpret_cast<uint32_t*>(y + c1) = b.y;
             }
+            if (l == 0) (which == 1 ? a.k_scale : a.v_scale)[cache_row] = rq.scale;
           }
-          if (l == 0) (row_which == 1 ? a.k_scale : a.v_scale)[cache_row] = rq.scale;
+          return;
         }
-        continue;
       }
     }
-    if (!live || !in || (CACHE != kCacheNone && row_which != 0 && slot < 0)) continue;
+    if (!live || !in || (CACHE != kCacheNone && which != 0 && slot < 0)) return;
     T* y;
-    if (row_which == 0) {
-      y = static_cast<T*>(a.q_out) + token * a.q_out_stride + static_cast<int64_t>(row_at) * a.head_dim;
+    if (which == 0) {
+      y = static_cast<T*>(a.q_out) + token * a.q_out_stride + static_cast<int64_t>(at) * a.head_dim;
     } else if (CACHE == kCacheNone) {
-      y = static_cast<T*>(a.k_out) + token * a.k_out_stride + static_cast<int64_t>(row_at) * a.head_dim;
+      y = static_cast<T*>(a.k_out) + token * a.k_out_stride + static_cast<int64_t>(at) * a.head_dim;
     } else {
-      y = static_cast<T*>(row_which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
+      y = static_cast<T*>(which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
     }
     Chunk<T, VEC> o0, o1;
     o0.narrow(f0);
     o1.narrow(f1);
     o0.store(y + c0);
     o1.store(y + c1);
+  };
+
+  // the bounds are the same for the whole warp: its lanes meet in the reductions
+  for (int first = begin; first < heads; first += kDepth * step, h += kDepth * step) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (first + d * step < heads) {
+        const Chunk<T, VEC> r0 = x0[d], r1 = x1[d];
+        fetch(h + (d + kDepth) * step, x0[d], x1[d]);
+        work_on(first + d * step, h + d * step, r0, r1);
+      }
+    }
   }
 }
 
