@@ -74,7 +74,7 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) {
 
 constexpr int kNormRopeBlock = 128;
 #ifndef DQ_NR_CTAS
-#define DQ_NR_CTAS 4
+#define DQ_NR_CTAS 5
 #endif
 #ifndef DQ_NR_DEPTH
 #define DQ_NR_DEPTH 2
@@ -252,12 +252,28 @@ struct Chunk {
   }
 };
 
+// VEC weights from channel c on, as binary32.
 template <int VEC>
 __device__ __forceinline__ void load_weights(const void* p, int dtype, int c, float2 (&w)[VEC / 2]) {
+  if (p == nullptr) {
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i)
-    w[i] = p == nullptr ? make_float2(1.0f, 1.0f)
-                        : make_float2(load_param(p, dtype, c + 2 * i), load_param(p, dtype, c + 2 * i + 1));
+    for (int i = 0; i < VEC / 2; ++i) w[i] = make_float2(1.0f, 1.0f);
+  } else if (dtype == kF32) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c) + i);
+      w[2 * i] = make_float2(v.x, v.y);
+      w[2 * i + 1] = make_float2(v.z, v.w);
+    }
+  } else if (dtype == kF16) {
+    Chunk<__half, VEC> x;
+    x.load(static_cast<const __half*>(p) + c);
+    x.widen(w);
+  } else {
+    Chunk<__nv_bfloat16, VEC> x;
+    x.load(static_cast<const __nv_bfloat16*>(p) + c);
+    x.widen(w);
+  }
 }
 
 // A warp takes one token and loops over its head rows, 32 / L rows at a time,
@@ -270,15 +286,18 @@ __device__ __forceinline__ void load_weights(const void* p, int dtype, int c, fl
 template <typename T, int VEC, int CACHE>
 __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int H = VEC / 2;
+  __shared__ __align__(16) float s_cos[kNormRopeBlock / 32][DQ_MAX_HEAD_DIM / 2];
+  __shared__ __align__(16) float s_sin[kNormRopeBlock / 32][DQ_MAX_HEAD_DIM / 2];
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31;
-  const int64_t work = static_cast<int64_t>(blockIdx.x) * (kNormRopeBlock / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t work = static_cast<int64_t>(blockIdx.x) * (kNormRopeBlock / 32) + warp;
   const int64_t token = work / a.parts;
   if (token >= a.tokens) return;
   const int part = static_cast<int>(work - token * a.parts);
   const int lanes = 1 << a.lane_shift, rows_at_once = 32 >> a.lane_shift, l = lane & (lanes - 1);
-  const int heads = a.q_heads + a.kv_heads * (CACHE == kCacheNone ? 1 : 2);
+  const int normed_rows = a.q_heads + a.kv_heads;
+  const int heads = normed_rows + (CACHE == kCacheNone ? 0 : a.kv_heads);
 
   // the lane's chunks
   const int half = a.rope_dim / 2, pair_chunks = a.interleaved ? 0 : half / VEC;
@@ -286,63 +305,59 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
   const int c0 = (split ? l : pair_chunks + 2 * (l - pair_chunks) + pair_chunks) * VEC;
   const int c1 = split ? c0 + half : c0 + VEC;
   const bool in = c1 < a.head_dim;
-
-  const T* q = static_cast<const T*>(a.q) + token * a.q_stride + c0;
-  const T* k = static_cast<const T*>(a.k) + token * a.k_stride + c0;
-  const T* v = static_cast<const T*>(a.v) + (CACHE == kCacheNone ? 0 : token * a.v_stride) + c0;
   const int apart = c1 - c0;
-  // row `h` of the token: 0 query, 1 key, 2 value, and its number there
-  const auto kind = [&](int h) -> int { return h < a.q_heads ? 0 : (h < a.q_heads + a.kv_heads ? 1 : 2); };
-  const auto number = [&](int h, int which) -> int {
-    return h - (which == 0 ? 0 : (which == 1 ? a.q_heads : a.q_heads + a.kv_heads));
+  const int step = rows_at_once * a.parts, begin = part * rows_at_once;
+
+  // Rows 0 .. heads - 1 of the token are its queries, keys and values. A place
+  // walks over them `step` rows at a time; only where a kind ends is it looked up.
+  struct Place {
+    int row, which, end;
+    const T* p;
   };
-  const int step = rows_at_once * a.parts;
-  const int begin = part * rows_at_once;
-  int h = begin + (lane >> a.lane_shift);
+  const auto find = [&](Place& x) {
+    x.which = x.row < a.q_heads ? 0 : (x.row < normed_rows ? 1 : 2);
+    x.end = x.which == 0 ? a.q_heads : (x.which == 1 ? normed_rows : heads);
+    const int at = x.row - (x.which == 0 ? 0 : (x.which == 1 ? a.q_heads : normed_rows));
+    const T* base = static_cast<const T*>(x.which == 0 ? a.q : (x.which == 1 ? a.k : a.v));
+    x.p = base + token * (x.which == 0 ? a.q_stride : (x.which == 1 ? a.k_stride : a.v_stride)) + at * a.head_dim + c0;
+  };
+  Place from;
+  from.row = begin + (lane >> a.lane_shift);
+  find(from);
   Chunk<T, VEC> x0[kDepth], x1[kDepth];
-  const auto fetch = [&](int row, Chunk<T, VEC>& y0, Chunk<T, VEC>& y1) {
-    if (row < heads && in) {
-      const int which = kind(row);
-      const T* p = (which == 0 ? q : (which == 1 ? k : v)) + number(row, which) * a.head_dim;
-      y0.load(p);
-      y1.load(p + apart);
+  const auto fetch = [&](Chunk<T, VEC>& y0, Chunk<T, VEC>& y1) {
+    if (from.row < heads && in) {
+      y0.load(from.p);
+      y1.load(from.p + apart);
     } else {
       y0.clear();
       y1.clear();
     }
+    from.row += step;
+    from.p += step * a.head_dim;
+    if (from.row >= from.end && from.row < heads) find(from);
   };
 #pragma unroll
-  for (int d = 0; d < kDepth; ++d) fetch(h + d * step, x0[d], x1[d]);
+  for (int d = 0; d < kDepth; ++d) fetch(x0[d], x1[d]);
 
-  // Angles: angle i turns channels (i, i + rope_dim / 2), or (2i, 2i + 1). Lane j
-  // computes angles j, j + 32, ... and every lane picks its own VEC.
-  float2 cs[H], sn[H];
-#pragma unroll
-  for (int i = 0; i < H; ++i) {
-    cs[i] = make_float2(1.0f, 1.0f);
-    sn[i] = make_float2(0.0f, 0.0f);
-  }
+  // Angles: angle i turns channels (i, i + rope_dim / 2), or (2i, 2i + 1). The
+  // lanes compute them once for the token's rows, then each picks its own VEC.
+  float2 cs[H], sn[H], ns[H];
   if (half > 0) {
     const int32_t pos = a.positions[token];
+    for (int i = lane; i < half; i += 32) rope_angle(pos, a.inv_freq[i], s_cos[warp][i], s_sin[warp][i]);
+    __syncwarp();
+  }
 #pragma unroll
-    for (int set = 0; set < DQ_MAX_HEAD_DIM / 64; ++set) {
-      if (32 * set < half) {
-        float c = 1.0f, s = 0.0f;
-        if (32 * set + lane < half) rope_angle(pos, a.inv_freq[32 * set + lane], c, s);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          // split: c0 + i; interleaved: c0 / 2 ... of the first chunk, then c1 / 2 ... of the second
-          const int want = a.interleaved ? (i < H ? c0 / 2 + i : c1 / 2 + i - H) : c0 + i;
-          const float cw = __shfl_sync(0xffffffffu, c, want & 31), sw = __shfl_sync(0xffffffffu, s, want & 31);
-          const bool mine = (want >> 5) == set && want < half && (a.interleaved || split);
-          float& cd = i & 1 ? cs[i / 2].y : cs[i / 2].x;
-          float& sd = i & 1 ? sn[i / 2].y : sn[i / 2].x;
-          if (mine) {
-            cd = cw;
-            sd = sw;
-          }
-        }
-      }
+  for (int i = 0; i < VEC; ++i) {
+    // split: c0 + i; interleaved: c0 / 2 ... of the first chunk, then c1 / 2 ... of the second
+    const int want = a.interleaved ? (i < H ? c0 / 2 + i : c1 / 2 + i - H) : c0 + i;
+    const bool turned = want < half && (a.interleaved || split);
+    const float c = turned ? s_cos[warp][want] : 1.0f, z = turned ? s_sin[warp][want] : 0.0f;
+    if (i & 1) {
+      cs[i / 2].y = c, sn[i / 2].y = z, ns[i / 2].y = -z;
+    } else {
+      cs[i / 2].x = c, sn[i / 2].x = z, ns[i / 2].x = -z;
     }
   }
   int64_t slot = -1, page_row = 0;
@@ -354,17 +369,41 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
       page_row = page * a.kv_heads * a.page_size + (slot - page * a.page_size);
     }
   }
-  int loaded = -1;
-  float2 w0[H], w1[H];
 
-  const auto work_on = [&](int first, int row, const Chunk<T, VEC>& r0, const Chunk<T, VEC>& r1) {
+  // where the rows go: elements (codes: bytes) of q_out, k_out or a cache
+  Place to;
+  to.row = begin + (lane >> a.lane_shift);
+  char* out = nullptr;
+  int64_t out_step = 0, cache_row = 0;
+  float2 w0[H], w1[H];
+  const auto aim = [&]() {
+    find(to);
+    const int at = to.row - (to.which == 0 ? 0 : (to.which == 1 ? a.q_heads : normed_rows));
+    if (to.which == 0) {
+      out = static_cast<char*>(a.q_out) + (token * a.q_out_stride + at * a.head_dim + c0) * sizeof(T);
+      out_step = static_cast<int64_t>(step) * a.head_dim * sizeof(T);
+    } else if (CACHE == kCacheNone) {
+      out = static_cast<char*>(a.k_out) + (token * a.k_out_stride + at * a.head_dim + c0) * sizeof(T);
+      out_step = static_cast<int64_t>(step) * a.head_dim * sizeof(T);
+    } else {
+      constexpr int kElem = CACHE == kCacheInt8 ? 1 : sizeof(T);
+      cache_row = page_row + static_cast<int64_t>(at) * a.page_size;
+      out = static_cast<char*>(to.which == 1 ? a.k_cache : a.v_cache) + (cache_row * a.head_dim + c0) * kElem;
+      out_step = static_cast<int64_t>(step) * a.page_size * a.head_dim * kElem;
+    }
+    if (to.which != 2 && in) {
+      const void* w = to.which == 0 ? a.q_weight : a.k_weight;
+      load_weights<VEC>(w, a.weight_dtype, c0, w0);
+      load_weights<VEC>(w, a.weight_dtype, c1, w1);
+    }
+  };
+  aim();
+
+  const auto work_on = [&](int first, const Chunk<T, VEC>& r0, const Chunk<T, VEC>& r1) {
     float2 f0[H], f1[H];
     r0.widen(f0);
     r1.widen(f1);
-    const bool live = row < heads;
-    const int which = live ? kind(row) : (CACHE == kCacheNone ? 1 : 2), at = number(row, which);
-    float r = 1.0f;
-    if (first < a.q_heads + a.kv_heads) {  // some row of the warp is normed
+    if (first < normed_rows) {  // some row of the warp is normed
       float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < H; ++i) sum2 = __ffma2_rn(f0[i], f0[i], __ffma2_rn(f1[i], f1[i], sum2));
@@ -373,13 +412,8 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
       for (int o = 1; o < 32; o *= 2) {
         if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
-      if (which != 2) {
-        if (loaded != which && in) {  // at the first row, and where the queries end
-          loaded = which;
-          load_weights<VEC>(which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c0, w0);
-          load_weights<VEC>(which == 0 ? a.q_weight : a.k_weight, a.weight_dtype, c1, w1);
-        }
-        r = rsqrtf(fmaf(sum, a.inv_dim, a.epsilon));
+      if (to.which != 2) {
+        const float r = rsqrtf(fmaf(sum, a.inv_dim, a.epsilon));
 #pragma unroll
         for (int i = 0; i < H; ++i) {
           f0[i] = __fmul2_rn(__fmul2_rn(f0[i], f2(r)), w0[i]);
@@ -397,13 +431,13 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
 #pragma unroll
           for (int i = 0; i < H; ++i) {
             const float2 y0 = f0[i], y1 = f1[i];
-            f0[i] = __ffma2_rn(y0, cs[i], __fmul2_rn(y1, make_float2(-sn[i].x, -sn[i].y)));
+            f0[i] = __ffma2_rn(y0, cs[i], __fmul2_rn(y1, ns[i]));
             f1[i] = __ffma2_rn(y1, cs[i], __fmul2_rn(y0, sn[i]));
           }
         }
       }
     }
-    const int64_t cache_row = page_row + static_cast<int64_t>(at) * a.page_size;
+    const bool live = to.row < heads && in && (CACHE == kCacheNone || to.which == 0 || slot >= 0);
     if constexpr (CACHE == kCacheInt8) {
       if (first + rows_at_once > a.q_heads) {  // some row of the warp becomes codes
         float top = 0.0f;
@@ -414,10 +448,9 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
         for (int o = 1; o < 32; o *= 2) {
           if (o < lanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
-        if (which != 0) {
-          if (live && slot >= 0 && in) {
-            RowQuant rq = make_sym<127>(top);
-            int8_t* y = static_cast<int8_t*>(which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
+        if (to.which != 0) {
+          if (live) {
+            const RowQuant rq = make_sym<127>(top);
             uint32_t bits[8];
             const auto codes = [&](const float(&f)[8]) -> uint2 {
               if (rq.zero_scale) return make_uint2(0u, 0u);
@@ -431,44 +464,40 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
             if constexpr (VEC == 8) {
               const float a0[8] = {f0[0].x, f0[0].y, f0[1].x, f0[1].y, f0[2].x, f0[2].y, f0[3].x, f0[3].y};
               const float a1[8] = {f1[0].x, f1[0].y, f1[1].x, f1[1].y, f1[2].x, f1[2].y, f1[3].x, f1[3].y};
-              *reinterpret_cast<uint2*>(y + c0) = codes(a0);
-              *reinterpret_cast<uint2*>(y + c1) = codes(a1);
+              *reinterpret_cast<uint2*>(out) = codes(a0);
+              *reinterpret_cast<uint2*>(out + apart) = codes(a1);
             } else {
               const float f[8] = {f0[0].x, f0[0].y, f0[1].x, f0[1].y, f1[0].x, f1[0].y, f1[1].x, f1[1].y};
               const uint2 b = codes(f);
-              *reinterpret_cast<uint32_t*>(y + c0) = b.x;
-              *reinterpret_cast<uint32_t*>(y + c1) = b.y;
+              *reinterpret_cast<uint32_t*>(out) = b.x;
+              *reinterpret_cast<uint32_t*>(out + apart) = b.y;
             }
-            if (l == 0) (which == 1 ? a.k_scale : a.v_scale)[cache_row] = rq.scale;
+            if (l == 0) (to.which == 1 ? a.k_scale : a.v_scale)[cache_row] = rq.scale;
           }
           return;
         }
       }
     }
-    if (!live || !in || (CACHE != kCacheNone && which != 0 && slot < 0)) return;
-    T* y;
-    if (which == 0) {
-      y = static_cast<T*>(a.q_out) + token * a.q_out_stride + static_cast<int64_t>(at) * a.head_dim;
-    } else if (CACHE == kCacheNone) {
-      y = static_cast<T*>(a.k_out) + token * a.k_out_stride + static_cast<int64_t>(at) * a.head_dim;
-    } else {
-      y = static_cast<T*>(which == 1 ? a.k_cache : a.v_cache) + cache_row * a.head_dim;
-    }
+    if (!live) return;
     Chunk<T, VEC> o0, o1;
     o0.narrow(f0);
     o1.narrow(f1);
-    o0.store(y + c0);
-    o1.store(y + c1);
+    o0.store(reinterpret_cast<T*>(out));
+    o1.store(reinterpret_cast<T*>(out) + apart);
   };
 
   // the bounds are the same for the whole warp: its lanes meet in the reductions
-  for (int first = begin; first < heads; first += kDepth * step, h += kDepth * step) {
+  for (int first = begin; first < heads; first += kDepth * step) {
 #pragma unroll
     for (int d = 0; d < kDepth; ++d) {
       if (first + d * step < heads) {
         const Chunk<T, VEC> r0 = x0[d], r1 = x1[d];
-        fetch(h + (d + kDepth) * step, x0[d], x1[d]);
-        work_on(first + d * step, h + d * step, r0, r1);
+        fetch(x0[d], x1[d]);
+        work_on(first + d * step, r0, r1);
+        to.row += step;
+        out += out_step;
+        cache_row += static_cast<int64_t>(step) * a.page_size;
+        if (to.row >= to.end && to.row < heads) aim();
       }
     }
   }
@@ -495,6 +524,8 @@ dq_status launch_generic(const dq::NormRopeArgs& a, cudaStream_t stream) {
 // pairs (i, i + rope_dim / 2) lie in two chunks, the rest in pairs of chunks.
 bool vector_ok(const dq::NormRopeArgs& a, int cache, int vec) {
   const int bytes = 2 * vec, codes = vec;
+  const int weight_bytes = a.weight_dtype == dq::kF32 ? 16 : bytes;
+  if (!aligned(a.q_weight, weight_bytes) || !aligned(a.k_weight, weight_bytes)) return false;
   if (a.head_dim % (2 * vec) != 0) return false;
   if (a.interleaved ? a.rope_dim % vec != 0 : a.rope_dim / 2 % vec != 0) return false;
   const auto rows = [&](const void* p, int64_t stride) { return aligned(p, bytes) && stride % vec == 0; };
