@@ -76,10 +76,6 @@ constexpr int kNormRopeBlock = 128;
 #ifndef DQ_NR_CTAS
 #define DQ_NR_CTAS 5
 #endif
-#ifndef DQ_NR_DEPTH
-#define DQ_NR_DEPTH 2
-#endif
-constexpr int kDepth = DQ_NR_DEPTH;
 
 // Any head dimension, stride and alignment: one warp per (token, head row),
 // the row in registers (rotation pairs lane, lane + 32, ..., then the channels
@@ -281,8 +277,8 @@ __device__ __forceinline__ void load_weights(const void* p, int dtype, int c, fl
 // chunks of VEC channels, those that rotate with each other (i and i +
 // rope_dim / 2) or two neighbouring ones (interleaved pairs, channels past
 // rope_dim), so the rotation needs no exchange. A token's angles are computed
-// once, each by one lane, and handed round. kDepth sets of rows are in flight
-// while one is worked on. Few tokens: `parts` warps share one token's rows.
+// once, each by one lane, and handed round. The next rows are loaded before the
+// current ones are worked on. Few tokens: `parts` warps share one token's rows.
 template <typename T, int VEC, int CACHE>
 __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int H = VEC / 2;
@@ -291,10 +287,6 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
   pdl_launch_dependents();
   pdl_wait_primary();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t work = static_cast<int64_t>(blockIdx.x) * (kNormRopeBlock / 32) + warp;
-  const int64_t token = work / a.parts;
-  if (token >= a.tokens) return;
-  const int part = static_cast<int>(work - token * a.parts);
   const int lanes = 1 << a.lane_shift, rows_at_once = 32 >> a.lane_shift, l = lane & (lanes - 1);
   const int normed_rows = a.q_heads + a.kv_heads;
   const int heads = normed_rows + (CACHE == kCacheNone ? 0 : a.kv_heads);
@@ -306,7 +298,12 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
   const int c1 = split ? c0 + half : c0 + VEC;
   const bool in = c1 < a.head_dim;
   const int apart = c1 - c0;
-  const int step = rows_at_once * a.parts, begin = part * rows_at_once;
+  const int step = rows_at_once * a.parts;
+
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kNormRopeBlock / 32) + warp;
+  const int64_t token = unit / a.parts;
+  if (token >= a.tokens) return;
+  const int begin = static_cast<int>(unit - token * a.parts) * rows_at_once;
 
   // Rows 0 .. heads - 1 of the token are its queries, keys and values. A place
   // walks over them `step` rows at a time; only where a kind ends is it looked up.
@@ -324,21 +321,20 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
   Place from;
   from.row = begin + (lane >> a.lane_shift);
   find(from);
-  Chunk<T, VEC> x0[kDepth], x1[kDepth];
-  const auto fetch = [&](Chunk<T, VEC>& y0, Chunk<T, VEC>& y1) {
+  Chunk<T, VEC> x0, x1;
+  const auto fetch = [&]() {
     if (from.row < heads && in) {
-      y0.load(from.p);
-      y1.load(from.p + apart);
+      x0.load(from.p);
+      x1.load(from.p + apart);
     } else {
-      y0.clear();
-      y1.clear();
+      x0.clear();
+      x1.clear();
     }
     from.row += step;
     from.p += step * a.head_dim;
     if (from.row >= from.end && from.row < heads) find(from);
   };
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d) fetch(x0[d], x1[d]);
+  fetch();
 
   // Angles: angle i turns channels (i, i + rope_dim / 2), or (2i, 2i + 1). The
   // lanes compute them once for the token's rows, then each picks its own VEC.
@@ -487,19 +483,14 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
   };
 
   // the bounds are the same for the whole warp: its lanes meet in the reductions
-  for (int first = begin; first < heads; first += kDepth * step) {
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) {
-      if (first + d * step < heads) {
-        const Chunk<T, VEC> r0 = x0[d], r1 = x1[d];
-        fetch(x0[d], x1[d]);
-        work_on(first + d * step, r0, r1);
-        to.row += step;
-        out += out_step;
-        cache_row += static_cast<int64_t>(step) * a.page_size;
-        if (to.row >= to.end && to.row < heads) aim();
-      }
-    }
+  for (int first = begin; first < heads; first += step) {
+    const Chunk<T, VEC> r0 = x0, r1 = x1;
+    fetch();
+    work_on(first, r0, r1);
+    to.row += step;
+    out += out_step;
+    cache_row += static_cast<int64_t>(step) * a.page_size;
+    if (to.row >= to.end && to.row < heads) aim();
   }
 }
 
