@@ -5,9 +5,8 @@
 // For a head row x of D values with weight w:
 //   y = x * rsqrt(mean(x^2) + epsilon) * w
 //   (y[a], y[b]) <- (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
-// The angle pos * inv_freq is formed and reduced in binary64 (a binary32
-// product of a position of 100000 is off by up to 2^-8 of a radian), then
-// sincospi is taken of the remainder in [-1, 1], in units of pi.
+// The angle is reduced in integers (a binary32 product of inv_freq with a
+// position of 100000 is off by up to 2^-8 of a radian).
 #include <cmath>
 
 #include "dq.h"
@@ -48,11 +47,15 @@ struct NormRopeArgs {
 
 enum : int { kCacheNone = 0, kCacheSame = 1, kCacheInt8 = 2 };
 
-// cos and sin of pos * inv_freq: t is the angle in units of pi, reduced
-// exactly to [-1, 1] before the rounding to binary32.
+// An angle pos * inv_freq is pos * (inv_freq / 2 pi) turns, of which only the
+// fraction counts: with inv_freq / 2 pi as a 64-bit fraction of a turn (from its
+// binary64 value), the integer product with the position is exact modulo one
+// turn, and its upper half is the angle to 2^-32 of a turn.
 __device__ __forceinline__ void rope_angle(int32_t pos, float inv_freq, float& c, float& s) {
-  const double t = static_cast<double>(pos) * static_cast<double>(inv_freq) * 0.31830988618379067154;
-  sincospif(static_cast<float>(t - 2.0 * rint(0.5 * t)), &s, &c);
+  const double t = static_cast<double>(inv_freq) * 0.15915494309189533577;  // 1 / (2 pi)
+  const uint64_t turns = static_cast<uint64_t>((t - floor(t)) * 0x1p63) << 1;
+  const uint64_t part = static_cast<uint64_t>(static_cast<int64_t>(pos)) * turns;
+  sincospif(static_cast<float>(static_cast<int32_t>(part >> 32)) * 0x1p-31f, &s, &c);
 }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
@@ -279,7 +282,7 @@ __device__ __forceinline__ void load_weights(const void* p, int dtype, int c, fl
 // rope_dim), so the rotation needs no exchange. A token's angles are computed
 // once, each by one lane, and handed round. The next rows are loaded before the
 // current ones are worked on. Few tokens: `parts` warps share one token's rows.
-template <typename T, int VEC, int CACHE>
+template <typename T, int VEC, int CACHE, int LANES>
 __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int H = VEC / 2;
   __shared__ __align__(16) float s_cos[kNormRopeBlock / 32][DQ_MAX_HEAD_DIM / 2];
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
   pdl_launch_dependents();
   pdl_wait_primary();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lanes = 1 << a.lane_shift, rows_at_once = 32 >> a.lane_shift, l = lane & (lanes - 1);
+  const int lanes = LANES ? LANES : 1 << a.lane_shift, rows_at_once = 32 / lanes, l = lane & (lanes - 1);
   const int normed_rows = a.q_heads + a.kv_heads;
   const int heads = normed_rows + (CACHE == kCacheNone ? 0 : a.kv_heads);
 
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
     x.p = base + token * (x.which == 0 ? a.q_stride : (x.which == 1 ? a.k_stride : a.v_stride)) + at * a.head_dim + c0;
   };
   Place from;
-  from.row = begin + (lane >> a.lane_shift);
+  from.row = begin + (lane / lanes);
   find(from);
   Chunk<T, VEC> x0, x1;
   const auto fetch = [&]() {
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
 
   // where the rows go: elements (codes: bytes) of q_out, k_out or a cache
   Place to;
-  to.row = begin + (lane >> a.lane_shift);
+  to.row = begin + (lane / lanes);
   char* out = nullptr;
   int64_t out_step = 0, cache_row = 0;
   float2 w0[H], w1[H];
@@ -405,7 +408,7 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
       for (int i = 0; i < H; ++i) sum2 = __ffma2_rn(f0[i], f0[i], __ffma2_rn(f1[i], f1[i], sum2));
       float sum = sum2.x + sum2.y;
 #pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
+      for (int o = 1; o < (LANES ? LANES : 32); o *= 2) {
         if (o < lanes) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       }
       if (to.which != 2) {
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(c
         for (int i = 0; i < H; ++i)
           top = max3(top, fmaxf(fabsf(f0[i].x), fabsf(f0[i].y)), fmaxf(fabsf(f1[i].x), fabsf(f1[i].y)));
 #pragma unroll
-        for (int o = 1; o < 32; o *= 2) {
+        for (int o = 1; o < (LANES ? LANES : 32); o *= 2) {
           if (o < lanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
         if (to.which != 0) {
@@ -526,9 +529,9 @@ bool vector_ok(const dq::NormRopeArgs& a, int cache, int vec) {
   return rows(a.v, a.v_stride) && aligned(a.k_cache, at) && aligned(a.v_cache, at);
 }
 
-template <typename T, int VEC, int CACHE>
+template <typename T, int VEC, int CACHE, int LANES>
 dq_status launch_vector(dq::NormRopeArgs a, cudaStream_t stream) {
-  void (*fn)(const dq::NormRopeArgs) = dq::norm_rope_kernel<T, VEC, CACHE>;
+  void (*fn)(const dq::NormRopeArgs) = dq::norm_rope_kernel<T, VEC, CACHE, LANES>;
   const int heads = a.q_heads + a.kv_heads * (CACHE == dq::kCacheNone ? 1 : 2);
   a.lane_shift = 0;
   while ((1 << a.lane_shift) * 2 * VEC < a.head_dim) ++a.lane_shift;
@@ -542,10 +545,17 @@ dq_status launch_vector(dq::NormRopeArgs a, cudaStream_t stream) {
   return dq_host::launch_programmatic(fn, a, static_cast<int>(grid), dq::kNormRopeBlock, 0, stream);
 }
 
+template <typename T, int VEC, int CACHE>
+dq_status by_lanes(const dq::NormRopeArgs& a, cudaStream_t stream) {
+  if (VEC == 8 && a.head_dim > 32 && a.head_dim <= 64) return launch_vector<T, 8, CACHE, 4>(a, stream);
+  if (VEC == 8 && a.head_dim > 64 && a.head_dim <= 128) return launch_vector<T, 8, CACHE, 8>(a, stream);
+  return launch_vector<T, VEC, CACHE, 0>(a, stream);
+}
+
 template <typename T, int CACHE>
 dq_status launch(const dq::NormRopeArgs& a, cudaStream_t stream) {
-  if (vector_ok(a, CACHE, 8)) return launch_vector<T, 8, CACHE>(a, stream);
-  if (vector_ok(a, CACHE, 4)) return launch_vector<T, 4, CACHE>(a, stream);
+  if (vector_ok(a, CACHE, 8)) return by_lanes<T, 8, CACHE>(a, stream);
+  if (vector_ok(a, CACHE, 4)) return by_lanes<T, 4, CACHE>(a, stream);
   return launch_generic<T, CACHE>(a, stream);
 }
 
