@@ -3,6 +3,7 @@
 #include "dq.h"
 #include "dq_launch.cuh"
 #include "w8a8_epilogue.cuh"
+#include "w8a8_linear_few.cuh"
 
 namespace dq {
 
@@ -42,8 +43,67 @@ dq_status launch_generic(const dq::LinearArgs& a, cudaStream_t stream) {
   return dq_host::launch_programmatic(fn, a, static_cast<int>(want < most ? want : most), 256, 0, stream);
 }
 
+// Few tokens: row blocks of 16 * (8 / KW) weight rows, K split over the CTAs of
+// a cluster.
+template <int ACT, int NT, int KW>
+dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
+  using Shape = dq::FewShape<NT, KW>;
+  auto fn = dq::w8a8_linear_few_kernel<ACT, NT, KW>;
+  const int device = dq_host::current_device();
+  if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
+  const int64_t sms = dq_host::sm_count(device);
+  const int64_t blocks = (a.n + Shape::kRows - 1) / Shape::kRows, token_blocks = (a.m + Shape::kTokens - 1) / Shape::kTokens;
+  const int64_t chunks = (a.k + Shape::kChunk - 1) / Shape::kChunk;
+  // the split whose CTAs spread most evenly over two per SM
+  int split = 1;
+  double best = 0.0;
+  for (int s = 1; s <= 8; s *= 2) {
+    if (s > chunks) break;
+    const int64_t ctas = blocks * token_blocks * s, waves = (ctas + 2 * sms - 1) / (2 * sms);
+    const double even = static_cast<double>(ctas) / static_cast<double>(waves * 2 * sms);
+    if (even > best + 0.02) {
+      best = even;
+      split = s;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks));
+  cfg.blockDim = dim3(dq::kFewThreads);
+  cfg.dynamicSmemBytes = Shape::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, fn, a, split) != cudaSuccess) {
+    cudaGetLastError();
+    return DQ_ERR_CUDA;
+  }
+  return dq_host::launch_status();
+}
+
 template <int ACT>
 dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
+  // 16-byte pieces of K
+  const bool pieces = a.k % 16 == 0 && aligned(a.a, 16) && aligned(a.b, 16);
+  if (pieces && a.n <= int64_t(1) << 28 && (a.m + 63) / 64 <= 65535) {
+    dq_status st = dq_host::kNotLaunchable;
+    if (a.m <= 8) {
+      st = launch_few<ACT, 1, 4>(a, stream);
+    } else if (a.m <= 16) {
+      st = launch_few<ACT, 2, 2>(a, stream);
+    } else if (a.m <= 32) {
+      st = launch_few<ACT, 4, 1>(a, stream);
+    } else {
+      st = launch_few<ACT, 8, 1>(a, stream);
+    }
+    if (st != dq_host::kNotLaunchable) return st;
+  }
   return launch_generic<ACT>(a, stream);
 }
 
