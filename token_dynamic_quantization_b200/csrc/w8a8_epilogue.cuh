@@ -63,4 +63,56 @@ __device__ __forceinline__ void store_one(void* p, int kind, int64_t e, float t)
   }
 }
 
+// Two 16-bit outputs in a word.
+__device__ __forceinline__ float2 unpack2(uint32_t w, int kind) {
+  if (kind == kOutF16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t pack2(float x, float y, int kind) {
+  if (kind == kOutF16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four neighbouring outputs of one row, in one access where rows allow it.
+// `broken`: the sum is incomplete (a bounded wait ran out), NaN marks it.
+template <int ACT>
+__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t n, int4 sum, bool has_bias, bool broken) {
+  if (n >= a.n) return;
+  const int acc[4] = {sum.x, sum.y, sum.z, sum.w};
+  const int64_t e = m * a.n + n;
+  const float sa = a.a_scale[m];
+  const bool whole = n + 4 <= a.n && a.vec_out;
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i < a.n) {
+      x[i] = linear_value<ACT>(acc[i], sa, a.b_scale[n + i], has_bias ? load_param(a.bias, a.bias_dtype, n + i) : 0.0f, has_bias);
+      if (broken) x[i] = __int_as_float(0x7fc00000);
+      if (!whole) {
+        if (a.residual != nullptr) x[i] = __fadd_rn(x[i], load_out(a.residual, a.out_kind, e + i));
+        store_one(a.out, a.out_kind, e + i, x[i]);
+      }
+    }
+  }
+  if (!whole) return;
+  if (a.out_kind == kOutF32) {
+    if (a.residual != nullptr) {
+      const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + e);
+      x[0] = __fadd_rn(x[0], r.x), x[1] = __fadd_rn(x[1], r.y), x[2] = __fadd_rn(x[2], r.z), x[3] = __fadd_rn(x[3], r.w);
+    }
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = make_float4(x[0], x[1], x[2], x[3]);
+    return;
+  }
+  if (a.residual != nullptr) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + e);
+    const float2 lo = unpack2(r.x, a.out_kind), hi = unpack2(r.y, a.out_kind);
+    x[0] = __fadd_rn(x[0], lo.x), x[1] = __fadd_rn(x[1], lo.y), x[2] = __fadd_rn(x[2], hi.x), x[3] = __fadd_rn(x[3], hi.y);
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) = make_uint2(pack2(x[0], x[1], a.out_kind), pack2(x[2], x[3], a.out_kind));
+}
+
 }  // namespace dq

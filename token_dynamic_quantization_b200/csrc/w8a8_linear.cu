@@ -4,6 +4,7 @@
 #include "dq_launch.cuh"
 #include "w8a8_epilogue.cuh"
 #include "w8a8_linear_few.cuh"
+#include "w8a8_linear_split.cuh"
 
 namespace dq {
 
@@ -31,6 +32,10 @@ __global__ void __launch_bounds__(256) w8a8_linear_generic_kernel(const LinearAr
 
 }  // namespace dq
 
+#ifndef DQ_FEW
+#define DQ_FEW 8
+#endif
+
 namespace {
 
 using dq_host::aligned;
@@ -41,6 +46,46 @@ dq_status launch_generic(const dq::LinearArgs& a, cudaStream_t stream) {
   const int64_t want = (a.m * a.n + 255) / 256;
   const int64_t most = static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * 64;
   return dq_host::launch_programmatic(fn, a, static_cast<int>(want < most ? want : most), 256, 0, stream);
+}
+
+// CTAs of a cluster among which K is split: the smallest number that comes
+// within 5 % of the most even load of `slots` resident CTAs.
+int even_split(int64_t tiles, int64_t pieces, int64_t slots) {
+  int split = 1;
+  double best = 0.0;
+  for (int s = 1; s <= 8 && s <= pieces; ++s) {
+    const int64_t ctas = tiles * s, waves = (ctas + slots - 1) / slots;
+    const double even = static_cast<double>(ctas) / static_cast<double>(waves * slots);
+    if (even > 1.05 * best) {
+      best = even;
+      split = s;
+    }
+  }
+  return split;
+}
+
+// A programmatic dependent launch in clusters of `cluster` CTAs along x.
+template <typename Kernel, typename... Args>
+dq_status launch_cluster(Kernel kernel, dim3 grid, int block, size_t smem, int cluster, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return DQ_ERR_CUDA;
+  }
+  return dq_host::launch_status();
 }
 
 // Few tokens: row blocks of 16 * (8 / KW) weight rows, K split over the CTAs of
@@ -54,37 +99,26 @@ dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
   const int64_t sms = dq_host::sm_count(device);
   const int64_t blocks = (a.n + Shape::kRows - 1) / Shape::kRows, token_blocks = (a.m + Shape::kTokens - 1) / Shape::kTokens;
   const int64_t chunks = (a.k + Shape::kChunk - 1) / Shape::kChunk;
-  // the split whose CTAs spread most evenly over two per SM
-  int split = 1;
-  double best = 0.0;
-  for (int s = 1; s <= 8; s *= 2) {
-    if (s > chunks) break;
-    const int64_t ctas = blocks * token_blocks * s, waves = (ctas + 2 * sms - 1) / (2 * sms);
-    const double even = static_cast<double>(ctas) / static_cast<double>(waves * 2 * sms);
-    if (even > best + 0.02) {
-      best = even;
-      split = s;
-    }
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks));
-  cfg.blockDim = dim3(dq::kFewThreads);
-  cfg.dynamicSmemBytes = Shape::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, fn, a, split) != cudaSuccess) {
-    cudaGetLastError();
-    return DQ_ERR_CUDA;
-  }
-  return dq_host::launch_status();
+  const int split = even_split(blocks * token_blocks, chunks, 2 * sms);
+  return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
+                        dq::kFewThreads, Shape::kSmem, split, stream, a, split);
+}
+
+// Up to a few hundred tokens: tiles of 128 weight rows by TOK tokens, K split
+// over the CTAs of a cluster.
+template <int ACT, int TOK>
+dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
+  using Shape = dq::SplitShape<TOK>;
+  auto fn = dq::w8a8_linear_split_kernel<ACT, TOK>;
+  const int device = dq_host::current_device();
+  CUtensorMap w, x;
+  if (!dq_host::make_map(&w, a.b, a.n, a.k, 128) || !dq_host::make_map(&x, a.a, a.m, a.k, TOK) ||
+      !dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem))
+    return dq_host::kNotLaunchable;
+  const int64_t blocks = (a.n + 127) / 128, token_blocks = (a.m + TOK - 1) / TOK;
+  const int split = even_split(blocks * token_blocks, (a.k + 127) / 128, dq_host::sm_count(device) * Shape::kCtas);
+  return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
+                        dq::kSplitThreads, Shape::kSmem, split, stream, w, x, a, split);
 }
 
 template <int ACT>
@@ -93,14 +127,20 @@ dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
   const bool pieces = a.k % 16 == 0 && aligned(a.a, 16) && aligned(a.b, 16);
   if (pieces && a.n <= int64_t(1) << 28 && (a.m + 63) / 64 <= 65535) {
     dq_status st = dq_host::kNotLaunchable;
-    if (a.m <= 8) {
-      st = launch_few<ACT, 1, 4>(a, stream);
+    if (a.m <= DQ_FEW) {
+      st = a.m <= 8 ? launch_few<ACT, 1, 4>(a, stream)
+                    : (a.m <= 16 ? launch_few<ACT, 2, 2>(a, stream)
+                                 : (a.m <= 32 ? launch_few<ACT, 4, 1>(a, stream) : launch_few<ACT, 8, 1>(a, stream)));
     } else if (a.m <= 16) {
-      st = launch_few<ACT, 2, 2>(a, stream);
+      st = launch_split<ACT, 16>(a, stream);
     } else if (a.m <= 32) {
-      st = launch_few<ACT, 4, 1>(a, stream);
+      st = launch_split<ACT, 32>(a, stream);
+    } else if (a.m <= 64) {
+      st = launch_split<ACT, 64>(a, stream);
+    } else if (a.m <= 128) {
+      st = launch_split<ACT, 128>(a, stream);
     } else {
-      st = launch_few<ACT, 8, 1>(a, stream);
+      st = launch_split<ACT, 256>(a, stream);
     }
     if (st != dq_host::kNotLaunchable) return st;
   }
