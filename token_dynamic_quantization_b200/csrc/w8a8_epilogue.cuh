@@ -77,42 +77,68 @@ __device__ __forceinline__ uint32_t pack2(float x, float y, int kind) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Four neighbouring outputs of one row, in one access where rows allow it.
-// `broken`: the sum is incomplete (a bounded wait ran out), NaN marks it.
-template <int ACT>
-__device__ __forceinline__ void finish4(const LinearArgs& a, int64_t m, int64_t n, int4 sum, bool has_bias, bool broken) {
-  if (n >= a.n) return;
-  const int acc[4] = {sum.x, sum.y, sum.z, sum.w};
-  const int64_t e = m * a.n + n;
-  const float sa = a.a_scale[m];
-  const bool whole = n + 4 <= a.n && a.vec_out;
-  float x[4];
+// Four neighbouring output columns from n on: what they need of the weights'
+// side, held in registers from before the sum is ready.
+struct Columns {
+  int64_t n;
+  int count;  // columns that exist
+  bool whole;  // one access per row serves all four
+  bool has_bias;
+  float scale[4], bias[4];
+
+  __device__ __forceinline__ Columns(const LinearArgs& a, int64_t first) : n(first) {
+    count = first >= a.n ? 0 : (first + 4 <= a.n ? 4 : static_cast<int>(a.n - first));
+    whole = count == 4 && a.vec_out;
+    has_bias = a.bias != nullptr;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i < a.n) {
-      x[i] = linear_value<ACT>(acc[i], sa, a.b_scale[n + i], has_bias ? load_param(a.bias, a.bias_dtype, n + i) : 0.0f, has_bias);
-      if (broken) x[i] = __int_as_float(0x7fc00000);
-      if (!whole) {
-        if (a.residual != nullptr) x[i] = __fadd_rn(x[i], load_out(a.residual, a.out_kind, e + i));
-        store_one(a.out, a.out_kind, e + i, x[i]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      scale[i] = i < count ? a.b_scale[n + i] : 0.0f;
+      bias[i] = i < count && has_bias ? load_param(a.bias, a.bias_dtype, n + i) : 0.0f;
     }
   }
-  if (!whole) return;
-  if (a.out_kind == kOutF32) {
+
+  // The residual of row m (zeros without one).
+  __device__ __forceinline__ float4 residual(const LinearArgs& a, int64_t m) const {
+    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (a.residual == nullptr || count == 0) return r;
+    const int64_t e = m * a.n + n;
+    if (whole) {
+      if (a.out_kind == kOutF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + e);
+      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + e);
+      const float2 lo = unpack2(w.x, a.out_kind), hi = unpack2(w.y, a.out_kind);
+      return make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    r.x = load_out(a.residual, a.out_kind, e);
+    if (count > 1) r.y = load_out(a.residual, a.out_kind, e + 1);
+    if (count > 2) r.z = load_out(a.residual, a.out_kind, e + 2);
+    if (count > 3) r.w = load_out(a.residual, a.out_kind, e + 3);
+    return r;
+  }
+
+  // Row m's outputs. `broken`: the sum is incomplete (a bounded wait ran out), NaN
+  // marks it.
+  template <int ACT>
+  __device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, float sa, int4 sum, float4 res, bool broken) const {
+    if (count == 0) return;
+    float x[4] = {linear_value<ACT>(sum.x, sa, scale[0], bias[0], has_bias), linear_value<ACT>(sum.y, sa, scale[1], bias[1], has_bias),
+                  linear_value<ACT>(sum.z, sa, scale[2], bias[2], has_bias), linear_value<ACT>(sum.w, sa, scale[3], bias[3], has_bias)};
     if (a.residual != nullptr) {
-      const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + e);
-      x[0] = __fadd_rn(x[0], r.x), x[1] = __fadd_rn(x[1], r.y), x[2] = __fadd_rn(x[2], r.z), x[3] = __fadd_rn(x[3], r.w);
+      x[0] = __fadd_rn(x[0], res.x), x[1] = __fadd_rn(x[1], res.y), x[2] = __fadd_rn(x[2], res.z), x[3] = __fadd_rn(x[3], res.w);
     }
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = make_float4(x[0], x[1], x[2], x[3]);
-    return;
+    if (broken) x[0] = x[1] = x[2] = x[3] = __int_as_float(0x7fc00000);
+    const int64_t e = m * a.n + n;
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < count) store_one(a.out, a.out_kind, e + i, x[i]);
+      }
+    } else if (a.out_kind == kOutF32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + e) = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) =
+          make_uint2(pack2(x[0], x[1], a.out_kind), pack2(x[2], x[3], a.out_kind));
+    }
   }
-  if (a.residual != nullptr) {
-    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + e);
-    const float2 lo = unpack2(r.x, a.out_kind), hi = unpack2(r.y, a.out_kind);
-    x[0] = __fadd_rn(x[0], lo.x), x[1] = __fadd_rn(x[1], lo.y), x[2] = __fadd_rn(x[2], hi.x), x[3] = __fadd_rn(x[3], hi.y);
-  }
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e) = make_uint2(pack2(x[0], x[1], a.out_kind), pack2(x[2], x[3], a.out_kind));
-}
+};
 
 }  // namespace dq

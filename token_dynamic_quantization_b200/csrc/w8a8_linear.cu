@@ -1,5 +1,8 @@
 // W8A8 product with bias, activation and residual in its epilogue
 // (dq_w8a8_linear).
+#include <atomic>
+#include <cstdio>
+
 #include "dq.h"
 #include "dq_launch.cuh"
 #include "w8a8_epilogue.cuh"
@@ -48,16 +51,51 @@ dq_status launch_generic(const dq::LinearArgs& a, cudaStream_t stream) {
   return dq_host::launch_programmatic(fn, a, static_cast<int>(want < most ? want : most), 256, 0, stream);
 }
 
-// CTAs of a cluster among which K is split: the smallest number that comes
-// within 5 % of the most even load of `slots` resident CTAs.
-int even_split(int64_t tiles, int64_t pieces, int64_t slots) {
+constexpr int kMaxSplit = 8;  // the portable cluster size
+
+// Clusters of 1 .. kMaxSplit CTAs of a kernel that fit the device at once (a
+// cluster stays within one GPC, so it is fewer than slots / size); asked once
+// per kernel and device. The answers are plain numbers that any thread would
+// write alike.
+template <typename Kernel>
+const int* resident_clusters(Kernel kernel, int device, int block, size_t smem, std::atomic<int> (&known)[kMaxSplit + 1],
+                             int (&out)[kMaxSplit + 1]) {
+  for (int s = 1; s <= kMaxSplit; ++s) {
+    int n = known[s].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(s) * 4096);
+      cfg.blockDim = dim3(block);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = s;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = dq_host::sm_count(device) / s;
+      }
+      known[s].store(n, std::memory_order_relaxed);
+    }
+    out[s] = n;
+  }
+  return out;
+}
+
+// CTAs of a cluster among which K is split: the number whose clusters take the
+// least time, in waves of resident clusters with K / split each; a larger one
+// has to gain 5 %.
+int best_split(int64_t tiles, int64_t pieces, const int* resident) {
   int split = 1;
   double best = 0.0;
-  for (int s = 1; s <= 8 && s <= pieces; ++s) {
-    const int64_t ctas = tiles * s, waves = (ctas + slots - 1) / slots;
-    const double even = static_cast<double>(ctas) / static_cast<double>(waves * slots);
-    if (even > 1.05 * best) {
-      best = even;
+  for (int s = 1; s <= kMaxSplit && s <= pieces; ++s) {
+    const double time = static_cast<double>((tiles + resident[s] - 1) / resident[s]) *
+                        (static_cast<double>((pieces + s - 1) / s) / static_cast<double>(pieces));
+    if (s == 1 || time < 0.95 * best) {
+      best = time;
       split = s;
     }
   }
@@ -96,10 +134,13 @@ dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
   auto fn = dq::w8a8_linear_few_kernel<ACT, NT, KW>;
   const int device = dq_host::current_device();
   if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
-  const int64_t sms = dq_host::sm_count(device);
   const int64_t blocks = (a.n + Shape::kRows - 1) / Shape::kRows, token_blocks = (a.m + Shape::kTokens - 1) / Shape::kTokens;
   const int64_t chunks = (a.k + Shape::kChunk - 1) / Shape::kChunk;
-  const int split = even_split(blocks * token_blocks, chunks, 2 * sms);
+  static std::atomic<int> known[dq_host::kMaxDevices][kMaxSplit + 1];
+  int resident[kMaxSplit + 1];
+  if (device < 0 || device >= dq_host::kMaxDevices) return dq_host::kNotLaunchable;
+  const int split = best_split(blocks * token_blocks, chunks,
+                               resident_clusters(fn, device, dq::kFewThreads, Shape::kSmem, known[device], resident));
   return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
                         dq::kFewThreads, Shape::kSmem, split, stream, a, split);
 }
@@ -116,7 +157,16 @@ dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
       !dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem))
     return dq_host::kNotLaunchable;
   const int64_t blocks = (a.n + 127) / 128, token_blocks = (a.m + TOK - 1) / TOK;
-  const int split = even_split(blocks * token_blocks, (a.k + 127) / 128, dq_host::sm_count(device) * Shape::kCtas);
+  static std::atomic<int> known[dq_host::kMaxDevices][kMaxSplit + 1];
+  int resident[kMaxSplit + 1];
+  if (device < 0 || device >= dq_host::kMaxDevices) return dq_host::kNotLaunchable;
+  const int split = best_split(blocks * token_blocks, (a.k + 127) / 128,
+                               resident_clusters(fn, device, dq::kSplitThreads, Shape::kSmem, known[device], resident));
+#ifdef DQ_DEBUG_SPLIT
+  printf("split %d of tiles %ld resident", split, (long)(blocks * token_blocks));
+  for (int s = 1; s <= kMaxSplit; ++s) printf(" %d", resident[s]);
+  printf("\n");
+#endif
   return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
                         dq::kSplitThreads, Shape::kSmem, split, stream, w, x, a, split);
 }

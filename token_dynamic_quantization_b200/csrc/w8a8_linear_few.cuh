@@ -20,6 +20,12 @@
 
 namespace dq {
 
+#ifndef PF
+#define PF 1
+#endif
+#ifndef RING
+#define RING 100
+#endif
 constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32;
 constexpr int kFewAhead = 4;                // K steps of 64 bytes in flight per warp
 
@@ -44,6 +50,11 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// `bytes` from p on (both multiples of 16) into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -64,6 +75,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) w8a8_linear_few_kernel(const L
   const int chunk0 = chunks * part / split, chunk1 = chunks * (part + 1) / split;
 
   pdl_launch_dependents();
+  // this CTA's weights on their way into L2 while the previous kernel ends: a
+  // prefetch returns nothing, and L2 is where that kernel's writes are seen
+  if (PF && threadIdx.x < Shape::kRows && n0 + threadIdx.x < a.n) {
+    const int64_t k0 = static_cast<int64_t>(chunk0) * kChunk;
+    const int64_t k1 = static_cast<int64_t>(chunk1) * kChunk < a.k ? static_cast<int64_t>(chunk1) * kChunk : a.k;
+    prefetch_l2(a.b + (n0 + threadIdx.x) * a.k + k0, static_cast<uint32_t>(k1 - k0));
+  }
 
   // weight rows g and g + 8 of the warp's set; rows past n repeat the last one
   const int64_t last = a.n - 1;

@@ -28,12 +28,11 @@ template <int TOK>
 struct SplitShape {
   static constexpr uint32_t kA = 128 * 128, kB = TOK * 128;  // bytes of a stage: weight rows, tokens
   static constexpr uint32_t kStage = kA + kB;
-  static constexpr int kCtas = TOK <= 64 ? 2 : 1;            // per SM
-  static constexpr int kStages = (kCtas == 2 ? 100 : 200) * 1024 / kStage;
+  static constexpr int kStages = 200 * 1024 / kStage;        // one CTA per SM
   static constexpr int kPitch = 132;                         // int32 parts [token][row]: 16-byte rows, no conflicts
   static constexpr uint32_t kSums = TOK * kPitch * 4;
   static constexpr uint32_t kRing = kStages * kStage > kSums ? kStages * kStage : kSums;
-  static constexpr size_t kSmem = 1024 + kRing + 256;
+  static constexpr size_t kSmem = 1024 + kRing + 256 + TOK * 4;
   static constexpr uint32_t kIdesc = i8_idesc(TOK);
   static constexpr uint32_t kCols = TOK < 32 ? 32 : TOK;     // TMEM columns
 };
@@ -52,6 +51,7 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ready + 1);
   volatile uint32_t* failed = tmem_slot + 1;
   volatile uint32_t* progress = tmem_slot + 2;
+  float* s_scale = reinterpret_cast<float*>(smem + Shape::kRing + 256);  // the tokens' scales
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = static_cast<int>(blockIdx.x) % split;
@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   const int s1 = static_cast<int>(static_cast<int64_t>(slices) * (part + 1) / split);
 
   if (threadIdx.x == 0) {
+    prefetch_map(&map_w);
+    prefetch_map(&map_x);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
@@ -82,7 +84,18 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
+  // this CTA's weights on their way into L2 while the previous kernel ends: a
+  // prefetch returns nothing, and L2 is where that kernel's writes are seen
+  if (PF && threadIdx.x >= 64 && n0 + threadIdx.x - 64 < a.n) {
+    const int64_t k0 = static_cast<int64_t>(s0) * 128, k1 = static_cast<int64_t>(s1) * 128 < a.k ? static_cast<int64_t>(s1) * 128 : a.k;
+    prefetch_l2(a.b + (n0 + threadIdx.x - 64) * a.k + k0, static_cast<uint32_t>(k1 - k0));
+  }
   pdl_wait_primary();
+
+  // what the epilogue needs of its four columns and of the tokens, asked for now
+  const int tokens = static_cast<int>(a.m - m0 < TOK ? a.m - m0 : TOK);
+  const Columns cols(a, n0 + 4 * lane);
+  for (int i = threadIdx.x; i < tokens; i += kSplitThreads) s_scale[i] = a.a_scale[m0 + i];
 
   if (warp == 0) {
     if (lane == 0) {
@@ -154,7 +167,6 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   }
 
   // each CTA of the cluster finishes every split-th token, four rows at a time
-  const int tokens = static_cast<int>(a.m - m0 < TOK ? a.m - m0 : TOK);
   const int mine = (tokens - part + split - 1) / split;
   bool broken = false;
   for (int r = 0; r < split; ++r) {
@@ -167,27 +179,40 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
     }
     broken |= v != 0u;
   }
-  const bool has_bias = a.bias != nullptr;
-  for (int i = threadIdx.x; i < mine * 32; i += kSplitThreads) {
-    const int tok = (i >> 5) * split + part, row = (i & 31) * 4;
-    const int64_t m = m0 + tok;
-    int4 sum = make_int4(0, 0, 0, 0);
-    const uint32_t at = smem_addr(sums) + (tok * Shape::kPitch + row) * 4;
-    for (int r = 0; r < split; ++r) {
-      int4 v;
-      if (split > 1) {
-        uint32_t remote;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(r));
-        asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(remote)
-                     : "memory");
-      } else {
-        v = *reinterpret_cast<const int4*>(sums + tok * Shape::kPitch + row);
+  // kBatch tokens at a time: their residuals and parts are all asked for before
+  // the first is used
+  constexpr int kBatch = 4, kWarps = kSplitThreads / 32;
+  for (int i0 = warp; i0 < mine; i0 += kBatch * kWarps) {
+    int4 sum[kBatch];
+    float4 res[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kWarps, tok = i * split + part;
+      sum[b] = make_int4(0, 0, 0, 0);
+      if (i < mine) {
+        res[b] = cols.residual(a, m0 + tok);
+        const uint32_t at = smem_addr(sums) + (tok * Shape::kPitch + 4 * lane) * 4;
+        for (int r = 0; r < split; ++r) {
+          int4 v;
+          if (split > 1) {
+            uint32_t remote;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(r));
+            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(remote)
+                         : "memory");
+          } else {
+            v = *reinterpret_cast<const int4*>(sums + tok * Shape::kPitch + 4 * lane);
+          }
+          sum[b].x += v.x, sum[b].y += v.y, sum[b].z += v.z, sum[b].w += v.w;
+        }
       }
-      sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
-    finish4<ACT>(a, m, n0 + row, sum, has_bias, broken);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kWarps, tok = i * split + part;
+      if (i < mine) cols.template finish<ACT>(a, m0 + tok, s_scale[tok], sum[b], res[b], broken);
+    }
   }
   if (split > 1) cluster_barrier();  // no CTA leaves while its part is being read
 }
