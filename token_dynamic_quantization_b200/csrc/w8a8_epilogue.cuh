@@ -97,32 +97,48 @@ struct Columns {
     }
   }
 
-  // The residual of row m (zeros without one).
-  __device__ __forceinline__ float4 residual(const LinearArgs& a, int64_t m) const {
-    float4 r = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // The residual of row m as it lies in memory, for finish(): nothing here waits
+  // for the load.
+  __device__ __forceinline__ uint4 residual(const LinearArgs& a, int64_t m) const {
+    uint4 r = make_uint4(0u, 0u, 0u, 0u);
     if (a.residual == nullptr || count == 0) return r;
     const int64_t e = m * a.n + n;
-    if (whole) {
-      if (a.out_kind == kOutF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + e);
-      const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + e);
-      const float2 lo = unpack2(w.x, a.out_kind), hi = unpack2(w.y, a.out_kind);
-      return make_float4(lo.x, lo.y, hi.x, hi.y);
+    if (a.out_kind == kOutF32) {
+      const uint32_t* p = static_cast<const uint32_t*>(a.residual) + e;
+      if (whole) return *reinterpret_cast<const uint4*>(p);
+      r.x = p[0];
+      if (count > 1) r.y = p[1];
+      if (count > 2) r.z = p[2];
+      if (count > 3) r.w = p[3];
+      return r;
     }
-    r.x = load_out(a.residual, a.out_kind, e);
-    if (count > 1) r.y = load_out(a.residual, a.out_kind, e + 1);
-    if (count > 2) r.z = load_out(a.residual, a.out_kind, e + 2);
-    if (count > 3) r.w = load_out(a.residual, a.out_kind, e + 3);
+    const uint16_t* p = static_cast<const uint16_t*>(a.residual) + e;
+    if (whole) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      return make_uint4(w.x, w.y, 0u, 0u);
+    }
+    r.x = p[0];
+    if (count > 1) r.y = p[1];
+    if (count > 2) r.z = p[2];
+    if (count > 3) r.w = p[3];
     return r;
+  }
+  __device__ __forceinline__ float4 widen(const LinearArgs& a, uint4 r) const {
+    if (a.out_kind == kOutF32)
+      return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
+    const float2 x = unpack2(whole ? r.x : r.x | r.y << 16, a.out_kind), y = unpack2(whole ? r.y : r.z | r.w << 16, a.out_kind);
+    return make_float4(x.x, x.y, y.x, y.y);
   }
 
   // Row m's outputs. `broken`: the sum is incomplete (a bounded wait ran out), NaN
   // marks it.
   template <int ACT>
-  __device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, float sa, int4 sum, float4 res, bool broken) const {
+  __device__ __forceinline__ void finish(const LinearArgs& a, int64_t m, float sa, int4 sum, uint4 raw, bool broken) const {
     if (count == 0) return;
     float x[4] = {linear_value<ACT>(sum.x, sa, scale[0], bias[0], has_bias), linear_value<ACT>(sum.y, sa, scale[1], bias[1], has_bias),
                   linear_value<ACT>(sum.z, sa, scale[2], bias[2], has_bias), linear_value<ACT>(sum.w, sa, scale[3], bias[3], has_bias)};
     if (a.residual != nullptr) {
+      const float4 res = widen(a, raw);
       x[0] = __fadd_rn(x[0], res.x), x[1] = __fadd_rn(x[1], res.y), x[2] = __fadd_rn(x[2], res.z), x[3] = __fadd_rn(x[3], res.w);
     }
     if (broken) x[0] = x[1] = x[2] = x[3] = __int_as_float(0x7fc00000);

@@ -35,6 +35,9 @@ __global__ void __launch_bounds__(256) w8a8_linear_generic_kernel(const LinearAr
 
 }  // namespace dq
 
+#ifndef FEW_SPLIT
+#define FEW_SPLIT 1
+#endif
 #ifndef DQ_FEW
 #define DQ_FEW 8
 #endif
@@ -85,6 +88,21 @@ const int* resident_clusters(Kernel kernel, int device, int block, size_t smem, 
   return out;
 }
 
+// The same for CTAs of which several share an SM: the split whose busiest SM has
+// the least to read, and of equal ones the largest (more loads in flight).
+int even_split(int64_t tiles, int64_t pieces, int64_t sms) {
+  int split = 1;
+  double best = 0.0;
+  for (int s = 1; s <= kMaxSplit && s <= pieces; ++s) {
+    const double time = static_cast<double>((tiles * s + sms - 1) / sms) * static_cast<double>((pieces + s - 1) / s);
+    if (s == 1 || time <= 1.02 * best) {
+      best = s == 1 || time < best ? time : best;
+      split = s;
+    }
+  }
+  return split;
+}
+
 // CTAs of a cluster among which K is split: the number whose clusters take the
 // least time, in waves of resident clusters with K / split each; a larger one
 // has to gain 5 %.
@@ -128,19 +146,15 @@ dq_status launch_cluster(Kernel kernel, dim3 grid, int block, size_t smem, int c
 
 // Few tokens: row blocks of 16 * (8 / KW) weight rows, K split over the CTAs of
 // a cluster.
-template <int ACT, int NT, int KW>
+template <int ACT, int NT, int RS, int KW>
 dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
-  using Shape = dq::FewShape<NT, KW>;
-  auto fn = dq::w8a8_linear_few_kernel<ACT, NT, KW>;
+  using Shape = dq::FewShape<NT, RS, KW>;
+  auto fn = dq::w8a8_linear_few_kernel<ACT, NT, RS, KW>;
   const int device = dq_host::current_device();
   if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
   const int64_t blocks = (a.n + Shape::kRows - 1) / Shape::kRows, token_blocks = (a.m + Shape::kTokens - 1) / Shape::kTokens;
   const int64_t chunks = (a.k + Shape::kChunk - 1) / Shape::kChunk;
-  static std::atomic<int> known[dq_host::kMaxDevices][kMaxSplit + 1];
-  int resident[kMaxSplit + 1];
-  if (device < 0 || device >= dq_host::kMaxDevices) return dq_host::kNotLaunchable;
-  const int split = best_split(blocks * token_blocks, chunks,
-                               resident_clusters(fn, device, dq::kFewThreads, Shape::kSmem, known[device], resident));
+  const int split = FEW_SPLIT ? FEW_SPLIT : even_split(blocks * token_blocks, chunks, dq_host::sm_count(device));
   return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
                         dq::kFewThreads, Shape::kSmem, split, stream, a, split);
 }
@@ -178,9 +192,11 @@ dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
   if (pieces && a.n <= int64_t(1) << 28 && (a.m + 63) / 64 <= 65535) {
     dq_status st = dq_host::kNotLaunchable;
     if (a.m <= DQ_FEW) {
-      st = a.m <= 8 ? launch_few<ACT, 1, 4>(a, stream)
-                    : (a.m <= 16 ? launch_few<ACT, 2, 2>(a, stream)
-                                 : (a.m <= 32 ? launch_few<ACT, 4, 1>(a, stream) : launch_few<ACT, 8, 1>(a, stream)));
+      st = a.m <= 8    ? launch_few<ACT, 1, 1, 4>(a, stream)
+           : a.m <= 16 ? launch_few<ACT, 2, 1, 4>(a, stream)
+           : a.m <= 32 ? launch_few<ACT, 4, FEW_RS2, FEW_KW2>(a, stream)
+           : a.m <= 48 ? launch_few<ACT, 6, FEW_RS2, FEW_KW2>(a, stream)
+                       : launch_few<ACT, 8, FEW_RS2, FEW_KW2>(a, stream);
     } else if (a.m <= 16) {
       st = launch_split<ACT, 16>(a, stream);
     } else if (a.m <= 32) {

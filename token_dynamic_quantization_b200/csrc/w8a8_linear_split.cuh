@@ -10,7 +10,7 @@
 //   warp 0      TMA producer: 128 bytes of K of the weight rows and the tokens
 //   warp 1      TMEM allocation; one lane issues tcgen05.mma.kind::i8
 //   warps 2-5   move the accumulator to shared memory, [token][row]
-//   all warps   sum the parts, epilogue, stores along the rows
+//               sum the parts, epilogue, stores along the rows
 // Every wait is bounded. A CTA whose sum is incomplete says so beside its part,
 // and the tokens that need it become NaN.
 #pragma once
@@ -61,6 +61,13 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   const int s0 = static_cast<int>(static_cast<int64_t>(slices) * part / split);
   const int s1 = static_cast<int>(static_cast<int64_t>(slices) * (part + 1) / split);
 
+  const auto load = [&](int i) {
+    const int s = i % kStages;
+    mbar_arrive_expect_tx(full + s, Shape::kStage);
+    uint8_t* at = smem + s * Shape::kStage;
+    tma_load_2d(at, &map_w, (s0 + i) * 128, static_cast<int>(n0), full + s);
+    tma_load_2d(at + Shape::kA, &map_x, (s0 + i) * 128, static_cast<int>(m0), full + s);
+  };
   if (threadIdx.x == 0) {
     prefetch_map(&map_w);
     prefetch_map(&map_x);
@@ -72,6 +79,9 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
     *failed = 0u;
     *progress = 0u;
     fence_mbarrier_init();
+    // the ring fills while the accumulator is being allocated
+    pdl_wait_primary();
+    for (int i = 0; i < kStages && i < s1 - s0; ++i) load(i);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
@@ -84,29 +94,20 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
-  // this CTA's weights on their way into L2 while the previous kernel ends: a
-  // prefetch returns nothing, and L2 is where that kernel's writes are seen
-  if (PF && threadIdx.x >= 64 && n0 + threadIdx.x - 64 < a.n) {
-    const int64_t k0 = static_cast<int64_t>(s0) * 128, k1 = static_cast<int64_t>(s1) * 128 < a.k ? static_cast<int64_t>(s1) * 128 : a.k;
-    prefetch_l2(a.b + (n0 + threadIdx.x - 64) * a.k + k0, static_cast<uint32_t>(k1 - k0));
-  }
   pdl_wait_primary();
 
-  // what the epilogue needs of its four columns and of the tokens, asked for now
+  // what the epilogue (warps 2-5) needs of its four columns and of the tokens,
+  // asked for now
   const int tokens = static_cast<int>(a.m - m0 < TOK ? a.m - m0 : TOK);
-  const Columns cols(a, n0 + 4 * lane);
-  for (int i = threadIdx.x; i < tokens; i += kSplitThreads) s_scale[i] = a.a_scale[m0 + i];
+  const Columns cols(a, warp < 2 ? a.n : n0 + 4 * lane);
+  for (int i = static_cast<int>(threadIdx.x) - 64; i >= 0 && i < tokens; i += 128) s_scale[i] = a.a_scale[m0 + i];
 
   if (warp == 0) {
     if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < s1 - s0; ++i, ++issued) {
-        const int s = i % kStages;
-        if (!mbar_wait_parity(empty + s, ((i / kStages) & 1u) ^ 1u)) break;
-        mbar_arrive_expect_tx(full + s, Shape::kStage);
-        uint8_t* at = smem + s * Shape::kStage;
-        tma_load_2d(at, &map_w, (s0 + i) * 128, static_cast<int>(n0), full + s);
-        tma_load_2d(at + Shape::kA, &map_x, (s0 + i) * 128, static_cast<int>(m0), full + s);
+      int issued = s1 - s0 < kStages ? s1 - s0 : kStages;
+      for (; issued < s1 - s0; ++issued) {
+        if (!mbar_wait_parity(empty + issued % kStages, ((issued / kStages) & 1u) ^ 1u)) break;
+        load(issued);
       }
       // nothing may still be landing when the ring is used for the parts
       for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i) {
@@ -181,10 +182,10 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   }
   // kBatch tokens at a time: their residuals and parts are all asked for before
   // the first is used
-  constexpr int kBatch = 4, kWarps = kSplitThreads / 32;
-  for (int i0 = warp; i0 < mine; i0 += kBatch * kWarps) {
+  constexpr int kBatch = 8, kWarps = 4;
+  for (int i0 = warp - 2; i0 >= 0 && i0 < mine; i0 += kBatch * kWarps) {
     int4 sum[kBatch];
-    float4 res[kBatch];
+    uint4 res[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int i = i0 + b * kWarps, tok = i * split + part;
