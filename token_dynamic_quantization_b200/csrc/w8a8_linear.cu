@@ -7,6 +7,7 @@
 #include "dq_launch.cuh"
 #include "w8a8_epilogue.cuh"
 #include "w8a8_linear_few.cuh"
+#include "w8a8_linear_pair.cuh"
 #include "w8a8_linear_split.cuh"
 
 namespace dq {
@@ -35,6 +36,9 @@ __global__ void __launch_bounds__(256) w8a8_linear_generic_kernel(const LinearAr
 
 }  // namespace dq
 
+#ifndef DQ_SPLIT_MOST
+#define DQ_SPLIT_MOST 256
+#endif
 #ifndef FEW_SPLIT
 #define FEW_SPLIT 1
 #endif
@@ -185,6 +189,28 @@ dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
                         dq::kSplitThreads, Shape::kSmem, split, stream, w, x, a, split);
 }
 
+// Many tokens: one pair of CTAs for every two SMs over the list of tiles.
+template <int ACT>
+dq_status launch_pair(const dq::LinearArgs& a, cudaStream_t stream) {
+  auto fn = dq::w8a8_linear_pair_kernel<ACT>;
+  const int device = dq_host::current_device();
+  CUtensorMap ma, mb128, mb64;
+  if (!dq_host::make_map(&ma, a.a, a.m, a.k, 128) || !dq_host::make_map(&mb128, a.b, a.n, a.k, 128) ||
+      !dq_host::make_map(&mb64, a.b, a.n, a.k, 64) ||
+      !dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, dq::kPairSmem))
+    return dq_host::kNotLaunchable;
+  const int64_t pairs = dq_host::sm_count(device) / 2;
+  dq::PairSched ps;
+  ps.n_tiles = (a.n + 255) / 256;
+  const int64_t tiles = (a.m + 255) / 256 * ps.n_tiles, rest = tiles % pairs;
+  const int64_t split = 2 * rest <= pairs ? rest : 0;  // halve the last ones when every half gets its own pair
+  ps.wide = tiles - split;
+  ps.items = tiles + split;
+  const int64_t clusters = ps.items < pairs ? ps.items : pairs;
+  return launch_cluster(fn, dim3(static_cast<unsigned>(2 * clusters)), dq::kPairThreads, dq::kPairSmem, 1, stream, ma,
+                        mb128, mb64, a, ps);
+}
+
 template <int ACT>
 dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
   // 16-byte pieces of K
@@ -205,8 +231,10 @@ dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
       st = launch_split<ACT, 64>(a, stream);
     } else if (a.m <= 128) {
       st = launch_split<ACT, 128>(a, stream);
-    } else {
+    } else if (a.m <= DQ_SPLIT_MOST) {
       st = launch_split<ACT, 256>(a, stream);
+    } else {
+      st = launch_pair<ACT>(a, stream);
     }
     if (st != dq_host::kNotLaunchable) return st;
   }

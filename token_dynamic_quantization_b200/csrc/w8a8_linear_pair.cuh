@@ -1,0 +1,310 @@
+// dq_w8a8_linear for many tokens: tiles of 256 tokens by 256 weight rows, each
+// by a pair of SMs (tcgen05 with cta_group::2).
+//
+// A single SM's 128 x 256 tile writes and reads 48 KB of operands per K slice
+// of 128 bytes, more than shared memory moves while the tensor core works on
+// it. A pair shares the weights: each SM holds its own 128 tokens and half of the
+// weight rows, 32 KB a slice, and the tensor cores read the other half from the
+// peer.
+//
+// Persistent: clusters of two CTAs walk a list of tiles; the last ones are halved
+// (256 x 128) when that evens out the last wave. Roles per CTA:
+//   warp 0      TMA producer: the CTA's tokens and its half of the weight rows;
+//               the copies complete on the leader's barrier
+//   warp 1      TMEM allocation; in the leader, one lane issues the MMAs for both
+//               SMs and frees both SMs' stages with multicast commits
+//   warps 2-9   epilogue of the CTA's 128 rows, two warps to a TMEM quarter; the
+//               int32 accumulator is double-buffered in TMEM (2 x 256 columns), so
+//               it overlaps the next tile's MMAs
+// Every wait is bounded; after one has run out the CTA's remaining tiles become NaN.
+#pragma once
+
+#include "dq_launch.cuh"
+#include "tcgen05_i8.cuh"
+#include "w8a8_epilogue.cuh"
+#include "w8a8_linear_few.cuh"
+
+namespace dq {
+
+constexpr int kPairEpilogueWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kPairEpilogueWarps;
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairA = 128 * 128, kPairB = 128 * 128;  // bytes of a stage in one CTA
+constexpr uint32_t kPairStage = kPairA + kPairB;
+constexpr uint32_t kPairCols = 512;
+constexpr uint32_t kPairIdescWide = i8_idesc(256, 256), kPairIdescNarrow = i8_idesc(128, 256);
+// ring, two buffers of 256 column scales and biases, barriers
+constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 2 * 2 * 256 * 4 + 256;
+
+struct PairSched {
+  int64_t n_tiles;  // 256-wide column tiles
+  int64_t wide;     // list items that are whole tiles
+  int64_t items;    // wide + 2 * (tiles split in two)
+};
+
+__device__ __forceinline__ void pair_item(const PairSched& ps, int64_t item, int64_t& m0, int64_t& n0, bool& wide) {
+  wide = item < ps.wide;
+  const int64_t t = wide ? item : ps.wide + (item - ps.wide) / 2, half = wide ? 0 : (item - ps.wide) & 1;
+  m0 = t / ps.n_tiles * 256;
+  n0 = t % ps.n_tiles * 256 + half * 128;
+}
+
+// A box into this CTA's shared memory, completing on a barrier of either CTA of
+// the pair (`bar`: its address in the cluster's window).
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(smem_addr(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_i8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives on the barrier at this place in both CTAs once every MMA issued so far
+// has completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+
+// 32 columns of one output row from the accumulator's words.
+template <int ACT>
+__device__ __forceinline__ void finish_row32(const LinearArgs& a, int64_t row, int64_t c0, const uint32_t (&r)[32],
+                                             const uint4* raw, float sa, const float* scale, const float* bias, bool vec) {
+  const bool has_bias = a.bias != nullptr;
+  const int64_t e = row * a.n + c0;
+  const bool narrow = a.out_kind != kOutF32;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {  // four columns
+    const float4 sb = *reinterpret_cast<const float4*>(scale + 4 * q), bb = *reinterpret_cast<const float4*>(bias + 4 * q);
+    float x[4] = {linear_value<ACT>(static_cast<int>(r[4 * q]), sa, sb.x, bb.x, has_bias),
+                  linear_value<ACT>(static_cast<int>(r[4 * q + 1]), sa, sb.y, bb.y, has_bias),
+                  linear_value<ACT>(static_cast<int>(r[4 * q + 2]), sa, sb.z, bb.z, has_bias),
+                  linear_value<ACT>(static_cast<int>(r[4 * q + 3]), sa, sb.w, bb.w, has_bias)};
+    if (!vec) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (c0 + 4 * q + i < a.n) {
+          if (a.residual != nullptr) x[i] = __fadd_rn(x[i], load_out(a.residual, a.out_kind, e + 4 * q + i));
+          store_one(a.out, a.out_kind, e + 4 * q + i, x[i]);
+        }
+      }
+    } else if (narrow) {
+      if (a.residual != nullptr) {
+        const uint4 w = raw[q / 2];
+        const float2 lo = unpack2(q & 1 ? w.z : w.x, a.out_kind), hi = unpack2(q & 1 ? w.w : w.y, a.out_kind);
+        x[0] = __fadd_rn(x[0], lo.x), x[1] = __fadd_rn(x[1], lo.y), x[2] = __fadd_rn(x[2], hi.x), x[3] = __fadd_rn(x[3], hi.y);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e + 4 * q) =
+          make_uint2(pack2(x[0], x[1], a.out_kind), pack2(x[2], x[3], a.out_kind));
+    } else {
+      float* o = static_cast<float*>(a.out) + e + 4 * q;
+      if (a.residual != nullptr) {
+        const float4 w = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + e + 4 * q);
+        x[0] = __fadd_rn(x[0], w.x), x[1] = __fadd_rn(x[1], w.y), x[2] = __fadd_rn(x[2], w.z), x[3] = __fadd_rn(x[3], w.w);
+      }
+      *reinterpret_cast<float4*>(o) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+  }
+}
+
+template <int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    w8a8_linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b128,
+                            const __grid_constant__ CUtensorMap map_b64, const LinearArgs a, const PairSched ps) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* col_scale = reinterpret_cast<float*>(smem + kPairStages * kPairStage);  // [2][256]
+  float* col_bias = col_scale + 2 * 256;                                         // [2][256]
+  uint64_t* full = reinterpret_cast<uint64_t*>(col_bias + 2 * 256);              // the leader's are used
+  uint64_t* empty = full + kPairStages;
+  uint64_t* acc_full = empty + kPairStages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2], the leader's are used
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t rank;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int64_t first_item = blockIdx.x / 2, step = gridDim.x / 2;
+  const int slices = static_cast<int>((a.k + 127) / 128);
+
+  if (threadIdx.x == 0) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b128);
+    prefetch_map(&map_b64);
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, 2 * kPairEpilogueWarps);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0u;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                 "r"(kPairCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // both CTAs' barriers exist before either touches the other's
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait_primary();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t slice = 0;
+      bool ok = true;
+      for (int64_t item = first_item; ok && item < ps.items; item += step) {
+        int64_t m0, n0;
+        bool wide;
+        pair_item(ps, item, m0, n0, wide);
+        const int rows_b = wide ? 128 : 64;  // this CTA's half of the weight rows
+        const CUtensorMap* map_b = wide ? &map_b128 : &map_b64;
+        for (int kt = 0; kt < slices; ++kt, ++slice) {
+          const uint32_t s = slice % kPairStages;
+          if (!wait_or_abort_for(empty + s, ((slice / kPairStages) & 1u) ^ 1u, abort_flag, kWaitLimitNs)) {
+            *abort_flag = 1u;
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * (kPairA + rows_b * 128));
+          const uint32_t bar = cluster_addr(full + s, 0);
+          uint8_t* at = smem + s * kPairStage;
+          tma_load_pair(at, &map_a, kt * 128, static_cast<int>(m0 + 128 * rank), bar);
+          tma_load_pair(at + kPairA, map_b, kt * 128, static_cast<int>(n0 + rows_b * rank), bar);
+        }
+      }
+      // no copy of either CTA may still be landing when the pair exits
+      if (rank == 0) {
+        for (uint32_t j = slice > kPairStages ? slice - kPairStages : 0; j < slice; ++j)
+          mbar_wait_parity(full + j % kPairStages, (j / kPairStages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t slice = 0;
+      bool ok = true;
+      int i = 0;
+      for (int64_t item = first_item; ok && item < ps.items; item += step, ++i) {
+        int64_t m0, n0;
+        bool wide;
+        pair_item(ps, item, m0, n0, wide);
+        const int acc = i & 1;
+        if (!wait_or_abort_for(acc_empty + acc, ((i >> 1) & 1) ^ 1u, abort_flag, kWaitLimitNs)) {
+          *abort_flag = 1u;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+        const uint32_t idesc = wide ? kPairIdescWide : kPairIdescNarrow;
+        for (int kt = 0; kt < slices; ++kt, ++slice) {
+          const uint32_t s = slice % kPairStages;
+          if (!wait_or_abort_for(full + s, (slice / kPairStages) & 1u, abort_flag, kWaitLimitNs)) {
+            *abort_flag = 1u;
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = smem_desc_k_sw128(smem + s * kPairStage);
+          const uint64_t bd = smem_desc_k_sw128(smem + s * kPairStage + kPairA);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) tc_mma_i8_pair(d, ad + 2 * kk, bd + 2 * kk, idesc, (kt | kk) != 0 ? 1u : 0u);
+          tc_commit_pair(empty + s);
+        }
+        if (ok) tc_commit_pair(acc_full + acc);
+      }
+      // the TMEM is freed below: every MMA issued has completed first
+      tc_commit_pair(mma_done);
+      mbar_wait_parity(mma_done, 0);
+    }
+    __syncwarp();
+  } else {
+    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;  // two warps per quarter, each half of the columns
+    const int et = threadIdx.x - 64;
+    bool dead = false;
+    int i = 0;
+    for (int64_t item = first_item; item < ps.items; item += step, ++i) {
+      int64_t m0, n0;
+      bool wide;
+      pair_item(ps, item, m0, n0, wide);
+      const int bn = wide ? 256 : 128;
+      const int acc = i & 1;
+      float* scale = col_scale + acc * 256;
+      float* bias = col_bias + acc * 256;
+      for (int j = et; j < bn; j += 32 * kPairEpilogueWarps) {
+        const bool in = n0 + j < a.n;
+        scale[j] = in ? a.b_scale[n0 + j] : 0.0f;
+        bias[j] = in && a.bias != nullptr ? load_param(a.bias, a.bias_dtype, n0 + j) : 0.0f;
+      }
+      const int64_t row = m0 + 128 * rank + 32 * quarter + lane;
+      const bool row_ok = row < a.m;
+      const float sa = row_ok ? a.a_scale[row] : 0.0f;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpilogueWarps) : "memory");
+      if (!dead) dead = !wait_or_abort_for(acc_full + acc, (i >> 1) & 1, abort_flag, kWaitLimitNs);
+      dead = __any_sync(0xffffffffu, dead);  // the warp agrees: the TMEM loads below are collective
+      tc_fence_after();
+      for (int c = half * (bn / 64); c < (half + 1) * (bn / 64); ++c) {
+        const int64_t c0 = n0 + 32 * c;
+        if (c0 >= a.n) break;  // the same for every lane
+        const bool vec = a.vec_out && c0 + 32 <= a.n;
+        if (dead) {
+          if (row_ok) {
+            for (int j = 0; j < 32 && c0 + j < a.n; ++j) store_one(a.out, a.out_kind, row * a.n + c0 + j, __int_as_float(0x7fc00000));
+          }
+          continue;
+        }
+        uint4 raw[4];
+        if (vec && row_ok && a.residual != nullptr && a.out_kind != kOutF32) {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.n + c0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) raw[q] = p[q];
+        }
+        uint32_t r[32];
+        tc_ld_32cols(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(acc * 256 + 32 * c), r);
+        if (row_ok) finish_row32<ACT>(a, row, c0, r, raw, sa, scale + 32 * c, bias + 32 * c, vec);
+      }
+      if (dead) *abort_flag = 1u;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(acc_empty + acc, 0)) : "memory");
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // no CTA leaves (or frees TMEM) while its peer still uses it
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPairCols) : "memory");
+  }
+}
+
+}  // namespace dq
