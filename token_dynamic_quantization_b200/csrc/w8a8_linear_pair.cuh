@@ -86,17 +86,23 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 // 32 columns of one output row from the accumulator's words.
 template <int ACT>
 __device__ __forceinline__ void finish_row32(const LinearArgs& a, int64_t row, int64_t c0, const uint32_t (&r)[32],
-                                             const uint4* raw, float sa, const float* scale, const float* bias, bool vec) {
+                                             const uint4 (&raw)[4], float sa, const float* scale, const float* bias, bool vec) {
   const bool has_bias = a.bias != nullptr;
   const int64_t e = row * a.n + c0;
   const bool narrow = a.out_kind != kOutF32;
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {  // four columns
-    const float4 sb = *reinterpret_cast<const float4*>(scale + 4 * q), bb = *reinterpret_cast<const float4*>(bias + 4 * q);
-    float x[4] = {linear_value<ACT>(static_cast<int>(r[4 * q]), sa, sb.x, bb.x, has_bias),
-                  linear_value<ACT>(static_cast<int>(r[4 * q + 1]), sa, sb.y, bb.y, has_bias),
-                  linear_value<ACT>(static_cast<int>(r[4 * q + 2]), sa, sb.z, bb.z, has_bias),
-                  linear_value<ACT>(static_cast<int>(r[4 * q + 3]), sa, sb.w, bb.w, has_bias)};
+  for (int q = 0; q < 8; ++q) {  // four columns, two to an instruction
+    const float4 sb = *reinterpret_cast<const float4*>(scale + 4 * q);
+    float2 lo = make_float2(__int2float_rn(static_cast<int>(r[4 * q])), __int2float_rn(static_cast<int>(r[4 * q + 1])));
+    float2 hi = make_float2(__int2float_rn(static_cast<int>(r[4 * q + 2])), __int2float_rn(static_cast<int>(r[4 * q + 3])));
+    lo = __fmul2_rn(lo, __fmul2_rn(f2(sa), make_float2(sb.x, sb.y)));
+    hi = __fmul2_rn(hi, __fmul2_rn(f2(sa), make_float2(sb.z, sb.w)));
+    if (has_bias) {
+      const float4 bb = *reinterpret_cast<const float4*>(bias + 4 * q);
+      lo = __fadd2_rn(lo, make_float2(bb.x, bb.y));
+      hi = __fadd2_rn(hi, make_float2(bb.z, bb.w));
+    }
+    float x[4] = {activate<ACT>(lo.x), activate<ACT>(lo.y), activate<ACT>(hi.x), activate<ACT>(hi.y)};
     if (!vec) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -108,8 +114,8 @@ __device__ __forceinline__ void finish_row32(const LinearArgs& a, int64_t row, i
     } else if (narrow) {
       if (a.residual != nullptr) {
         const uint4 w = raw[q / 2];
-        const float2 lo = unpack2(q & 1 ? w.z : w.x, a.out_kind), hi = unpack2(q & 1 ? w.w : w.y, a.out_kind);
-        x[0] = __fadd_rn(x[0], lo.x), x[1] = __fadd_rn(x[1], lo.y), x[2] = __fadd_rn(x[2], hi.x), x[3] = __fadd_rn(x[3], hi.y);
+        const float2 r0 = unpack2(q & 1 ? w.z : w.x, a.out_kind), r1 = unpack2(q & 1 ? w.w : w.y, a.out_kind);
+        x[0] = __fadd_rn(x[0], r0.x), x[1] = __fadd_rn(x[1], r0.y), x[2] = __fadd_rn(x[2], r1.x), x[3] = __fadd_rn(x[3], r1.y);
       }
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + e + 4 * q) =
           make_uint2(pack2(x[0], x[1], a.out_kind), pack2(x[2], x[3], a.out_kind));
@@ -266,6 +272,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int64_t row = m0 + 128 * rank + 32 * quarter + lane;
       const bool row_ok = row < a.m;
       const float sa = row_ok ? a.a_scale[row] : 0.0f;
+      // the residual of a chunk is asked for one chunk ahead, the first before the wait
+      const auto ask = [&](int c, uint4(&raw)[4]) {
+        const int64_t c0 = n0 + 32 * c;
+        if (a.residual != nullptr && a.out_kind != kOutF32 && row_ok && a.vec_out && c0 + 32 <= a.n && c < (half + 1) * (bn / 64)) {
+          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.n + c0);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) raw[q] = p[q];
+        }
+      };
+      uint4 next[4];
+      ask(half * (bn / 64), next);
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpilogueWarps) : "memory");
       if (!dead) dead = !wait_or_abort_for(acc_full + acc, (i >> 1) & 1, abort_flag, kWaitLimitNs);
       dead = __any_sync(0xffffffffu, dead);  // the warp agrees: the TMEM loads below are collective
@@ -281,11 +298,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           continue;
         }
         uint4 raw[4];
-        if (vec && row_ok && a.residual != nullptr && a.out_kind != kOutF32) {
-          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.n + c0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) raw[q] = p[q];
-        }
+        for (int q = 0; q < 4; ++q) raw[q] = next[q];
+        ask(c + 1, next);
         uint32_t r[32];
         tc_ld_32cols(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(acc * 256 + 32 * c), r);
         if (row_ok) finish_row32<ACT>(a, row, c0, r, raw, sa, scale + 32 * c, bias + 32 * c, vec);
