@@ -67,13 +67,13 @@ struct PagedShape {
   static constexpr int kRowBytes = kTokens * D * int(sizeof(C));
   static constexpr int kScaleBytes = kCodes ? 2 * 4 * kTokens : 0;
   static constexpr int kStageBytes = 2 * kRowBytes;
-  static constexpr int kFit = (224 * 1024 / kCtas - 2048) / kPagedWarps / (kStageBytes + kScaleBytes);
+  static constexpr int kJoin = kPagedWarps * (kHeads * D + 2 * kHeads) * 4;
+  static constexpr int kFit = (227 * 1024 / kCtas - 2048 - 256 - kJoin) / kPagedWarps / (kStageBytes + kScaleBytes);
   static constexpr int kStages = kFit < 2 ? 2 : (kFit > 8 ? 8 : kFit);
   static constexpr int kRings = kPagedWarps * kStages * kStageBytes;
   static constexpr int kScales = kPagedWarps * kStages * kScaleBytes;
-  static constexpr int kJoin = kPagedWarps * (kHeads * D + 2 * kHeads) * 4;
   static constexpr int kBarriers = kPagedWarps * kStages * 8;
-  static constexpr int kBody = kRings + kScales > kJoin ? kRings + kScales : kJoin;
+  static constexpr int kBody = kRings + kScales + kJoin;
   static constexpr size_t kSmem = 1024 + size_t(kBody) + kBarriers;  // 1024: alignment of the swizzle pattern
 };
 
@@ -203,9 +203,8 @@ struct Groups {
   int first_groups, count;
 };
 
-__device__ __forceinline__ Groups visible_groups(const PagedArgs& a, int64_t b) {
+__device__ __forceinline__ Groups visible_groups(const PagedArgs& a, int len) {
   const int64_t room = a.max_pages * a.page_size;
-  const int len = a.lengths[b];
   Groups v{len, 0, 0, 0, 0};
   if (len <= 0) {
     v.len = 0;
@@ -235,7 +234,7 @@ __device__ __forceinline__ int tiles_of(const Groups& v) {
 }
 template <int TT>
 __device__ __forceinline__ int64_t item_tiles(const PagedArgs& a, int64_t b) {
-  return tiles_of<TT>(visible_groups(a, b));
+  return tiles_of<TT>(visible_groups(a, a.lengths[b]));
 }
 
 __device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
@@ -305,8 +304,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
   constexpr int kStages = Shape::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  // the warps' rings and scales; once they are read, [warps][kHeads][D] and [warps][kHeads][2]
-  float* s_o = reinterpret_cast<float*>(smem);
+  // the warps' rings and scales; what they leave of an item, [warps][kHeads][D] and [warps][kHeads][2]
+  float* s_o = reinterpret_cast<float*>(smem + Shape::kRings + Shape::kScales);
   float* s_stat = s_o + kPagedWarps * kHeads * D;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -343,88 +342,26 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
   const int order = token_order<Shape::kBox>(g), order_even = token_order<Shape::kBox>(2 * t);
   const int order_odd = token_order<Shape::kBox>(2 * t + 1);
 
-  while (tile < tile_end) {
-    const Groups vis = visible_groups(a, seq);
-    const int64_t n = tiles_of<TT>(vis);
-    const int64_t item = (tile - base) / n;
-    const int64_t item_begin = base + item * n;
-    const int t0 = static_cast<int>(tile - item_begin);
-    const int t1 = static_cast<int>((item_begin + n < tile_end ? item_begin + n : tile_end) - item_begin);
-    const int kvh = static_cast<int>(item / a.head_sets);
+
+  // ---- the item at `tile`: its tokens, heads and rows of the page table
+  Groups vis;
+  int64_t n = 0, item = 0, item_begin = 0;
+  int t0 = 0, t1 = 0, kvh = 0, head0 = 0, heads = 0;
+  const int32_t* table = nullptr;
+  int len = a.lengths[seq], len_next = seq + 1 < a.batch ? a.lengths[seq + 1] : 0;
+  const auto enter = [&]() {
+    vis = visible_groups(a, len);
+    n = tiles_of<TT>(vis);
+    item = (tile - base) / n;
+    item_begin = base + item * n;
+    t0 = static_cast<int>(tile - item_begin);
+    t1 = static_cast<int>((item_begin + n < tile_end ? item_begin + n : tile_end) - item_begin);
+    kvh = static_cast<int>(item / a.head_sets);
     const int set = static_cast<int>(item - static_cast<int64_t>(kvh) * a.head_sets);
-    const int head0 = kvh * a.group + set * kHeads;                        // first query head
-    const int heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
-    const int32_t* table = a.page_table + seq * a.max_pages;
-
-    // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
-    // per k-step. Beside codes as two signed 8-bit digits, 256 q1 + q0, of a
-    // power of two times it, |.| <= 32639: channels down to 2^-7 (bf16; f16:
-    // 2^-4) of the head's largest are exact, the others within 2^-16 of it.
-    uint32_t qf[HT][KS][2];
-    float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      const bool on = 8 * ht + g < heads;
-      const T* q = static_cast<const T*>(a.q) + seq * a.q_stride + static_cast<int64_t>(head0 + 8 * ht + g) * D;
-      float mul = a.softmax_scale * kLog2e;
-      if constexpr (kCodes) {
-        uint2 w[KS];  // four channels each
-        uint32_t top = 0u;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          w[s] = on ? *reinterpret_cast<const uint2*>(q + (s / 4) * 64 + 16 * t + 4 * (s % 4)) : make_uint2(0u, 0u);
-          top = max(top, max(max(w[s].x & 0x7FFFu, (w[s].x >> 16) & 0x7FFFu), max(w[s].y & 0x7FFFu, (w[s].y >> 16) & 0x7FFFu)));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float largest = half_bits<T>(top);
-        int e = 0;
-        if (!isfinite(largest)) {
-          mul = NAN;
-        } else if (largest > 0.0f) {
-          e = 14 - ilogbf(largest);
-          if (scalbnf(largest, e) > 32639.0f) --e;
-          if (e > 126) e = 126;
-          mul = scalbnf(mul, -e);
-        }
-        const float f = scalbnf(1.0f, e);
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          int x[4] = {__float2int_rn(half_bits<T>(w[s].x & 0xFFFFu) * f), __float2int_rn(half_bits<T>(w[s].x >> 16) * f),
-                      __float2int_rn(half_bits<T>(w[s].y & 0xFFFFu) * f), __float2int_rn(half_bits<T>(w[s].y >> 16) * f)};
-          uint32_t hi = 0u, lo = 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int q1 = (x[i] + 128) >> 8;
-            hi |= (static_cast<uint32_t>(q1) & 255u) << (8 * i);
-            lo |= (static_cast<uint32_t>(x[i] - (q1 << 8)) & 255u) << (8 * i);
-          }
-          qf[ht][s][0] = hi;
-          qf[ht][s][1] = lo;
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const uint2 w = on ? *reinterpret_cast<const uint2*>(q + (s / 2) * 32 + 8 * t + 4 * (s % 2)) : make_uint2(0u, 0u);
-          qf[ht][s][0] = w.x;
-          qf[ht][s][1] = w.y;
-        }
-      }
-      q_mul[ht][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
-      q_mul[ht][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
-    }
-
-    float o[HT][KS][4], m[HT][2], l[HT][2];
-    float o_bias[HT][4];  // what the codes' bias of 128 has added to every channel of O
-    float v_top = 0.0f, v_mul = 1.0f;  // largest value scale so far, and the power of two that takes it below 2
-#pragma unroll
-    for (int ht = 0; ht < HT; ++ht) {
-      m[ht][0] = m[ht][1] = -INFINITY;
-      l[ht][0] = l[ht][1] = 0.0f;
-      o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < KS; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.0f;
-    }
+    head0 = kvh * a.group + set * kHeads;                                  // first query head
+    heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
+    table = a.page_table + seq * a.max_pages;
+  };
 
     // Token at place r of tile tl, and whether it is visible.
     const auto token_of = [&](int tl, int r, bool& seen) -> int {
@@ -497,35 +434,143 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       }
       if constexpr (kCodes) {
         if (lane < TT) {
-          const uint32_t dst = scales + st * Shape::kScaleBytes + lane * 4;
+          const uint32_t dst = scales + st * Shape::kScaleBytes + lane * 8;
           const uint32_t r = row < kRowBad ? row : 0u;
           copy_async4(dst, a.k_scale + r, row < kRowBad ? 4 : 0);
-          copy_async4(dst + TT * 4, a.v_scale + r, row < kRowBad ? 4 : 0);
+          copy_async4(dst + 4, a.v_scale + r, row < kRowBad ? 4 : 0);
         }
         copies_commit();
       }
     };
 
-    int tl = t0 + warp, st = 0;
-    fence_proxy_async_smem();
-    __syncthreads();  // the previous item's readers of the shared memory are done
-    fence_proxy_async_smem();
-    {
+    // The warp's first tiles of the item into its ring, and the item's queries as
+    // they lie in memory: asked for before the previous item is joined.
+    uint32_t in_page_next = 0u;
+    int32_t page_next = -2;
+    int st = 0;
+    uint2 qw[HT][KS];
+    const auto open = [&]() {
+      enter();
+      broken = false;
+      const int first = t0 + warp;
       int32_t page[kStages];
       uint32_t in_page[kStages];
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) page[i] = find_page(tl + i * kPagedWarps, in_page[i]);
+      for (int i = 0; i < kStages; ++i) page[i] = find_page(first + i * kPagedWarps, in_page[i]);
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+        const bool on = 8 * ht + g < heads;
+        const T* q = static_cast<const T*>(a.q) + seq * a.q_stride + static_cast<int64_t>(head0 + 8 * ht + g) * D;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const int c = kCodes ? (s / 4) * 64 + 16 * t + 4 * (s % 4) : (s / 2) * 32 + 8 * t + 4 * (s % 2);
+          qw[ht][s] = on ? *reinterpret_cast<const uint2*>(q + c) : make_uint2(0u, 0u);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kStages; ++i) {
-        if (tl + i * kPagedWarps < t1) {
+        if (first + i * kPagedWarps < t1) {
           issue(i, row_of(page[i], in_page[i]));
         } else if constexpr (kCodes) {
           copies_commit();
         }
       }
+      page_next = find_page(first + kStages * kPagedWarps, in_page_next);
+    };
+
+  open();
+  while (true) {
+    // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
+    // per k-step. Beside codes as two signed 8-bit digits, 256 q1 + q0, of a
+    // power of two times it, |.| <= 32639: channels down to 2^-7 (bf16; f16:
+    // 2^-4) of the head's largest are exact, the others within 2^-16 of it.
+    uint32_t qf[HT][KS][2];
+    float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+      float mul = fabsf(a.softmax_scale) * kLog2e;  // its sign goes into Q: the largest product has the largest score
+      if constexpr (kCodes) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 w = qw[ht][s];
+          top = max(top, max(max(w.x & 0x7FFFu, (w.x >> 16) & 0x7FFFu), max(w.y & 0x7FFFu, (w.y >> 16) & 0x7FFFu)));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float largest = half_bits<T>(top);
+        int e = 0;
+        if (!isfinite(largest)) {
+          mul = NAN;
+        } else if (largest > 0.0f) {
+          e = 14 - ilogbf(largest);
+          if (scalbnf(largest, e) > 32639.0f) --e;
+          if (e > 126) e = 126;
+          mul = scalbnf(mul, -e);
+        }
+        const float f = a.softmax_scale < 0.0f ? -scalbnf(1.0f, e) : scalbnf(1.0f, e);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 w = qw[ht][s];
+          int x[4] = {__float2int_rn(half_bits<T>(w.x & 0xFFFFu) * f), __float2int_rn(half_bits<T>(w.x >> 16) * f),
+                      __float2int_rn(half_bits<T>(w.y & 0xFFFFu) * f), __float2int_rn(half_bits<T>(w.y >> 16) * f)};
+          uint32_t hi = 0u, lo = 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int q1 = (x[i] + 128) >> 8;
+            hi |= (static_cast<uint32_t>(q1) & 255u) << (8 * i);
+            lo |= (static_cast<uint32_t>(x[i] - (q1 << 8)) & 255u) << (8 * i);
+          }
+          qf[ht][s][0] = hi;
+          qf[ht][s][1] = lo;
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          const uint2 w = qw[ht][s];
+          const uint32_t sign = a.softmax_scale < 0.0f ? 0x80008000u : 0u;
+          qf[ht][s][0] = w.x ^ sign;
+          qf[ht][s][1] = w.y ^ sign;
+        }
+      }
+      q_mul[ht][0] = __shfl_sync(0xffffffffu, mul, 8 * t);
+      q_mul[ht][1] = __shfl_sync(0xffffffffu, mul, 8 * t + 4);
     }
-    uint32_t in_page_next = 0u;
-    int32_t page_next = find_page(tl + kStages * kPagedWarps, in_page_next);
+
+    float o[HT][KS][4], m[HT][2], l[HT][2];
+    float o_bias[HT][4];  // what the codes' bias of 128 has added to every channel of O
+    // the power of two that takes the value scales so far below 2, and the scale
+    // from which on it has to move
+    float v_mul = 1.0f, v_limit = 0x1p-149f;
+    bool v_first = true;
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+      m[ht][0] = m[ht][1] = -INFINITY;
+      l[ht][0] = l[ht][1] = 0.0f;
+      o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.0f;
+    }
+
+    // groups whose tokens are all visible
+    const int inside_first = vis.first_groups == 0 && (vis.start & 15) == 0 ? 0 : vis.first_groups + ((vis.start & 15) != 0 ? 1 : 0);
+    const int inside_last = vis.first_groups + (vis.len >> 4) - (vis.start >> 4);
+    bool biased = false;  // O still holds the last tile's bias
+    const auto remove_bias = [&]() {
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+          o[ht][i][0] -= o_bias[ht][0];
+          o[ht][i][1] -= o_bias[ht][1];
+          o[ht][i][2] -= o_bias[ht][0];
+          o[ht][i][3] -= o_bias[ht][1];
+        }
+        o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
+      }
+    };
+    int tl = t0 + warp;
+    st = 0;
     for (; tl < t1; tl += kPagedWarps) {
       const uint32_t stage = ring + st * Shape::kStageBytes;
       if (!mbar_wait_parity(bars + st, (filled >> st) & 1u)) broken = true;
@@ -587,41 +632,58 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
           }
         }
       }
-      // ---- scores in log2, hidden tokens out
+      // ---- scores up to the heads' factors q_mul, hidden tokens out
+      const bool inside = tl * MT >= inside_first && tl * MT + MT <= inside_last;  // no token of the tile is hidden
       float vw[MT][2];
-      bool move = false, edge = false;
+      bool move = false;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int tok = 16 * mt + 8 * h + order;
-          bool seen;
-          token_of(tl, tok, seen);
-          edge |= !seen;
-          float k_mul = 1.0f;
           vw[mt][h] = 1.0f;
           if constexpr (kCodes) {
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(k_mul) : "r"(scales + st * Shape::kScaleBytes + tok * 4));
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vw[mt][h]) : "r"(scales + st * Shape::kScaleBytes + (TT + tok) * 4));
-            if (!seen) vw[mt][h] = 0.0f;
-            move |= vw[mt][h] > v_top;
-          }
+            float k_mul;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                         : "=f"(k_mul), "=f"(vw[mt][h])
+                         : "r"(scales + st * Shape::kScaleBytes + tok * 8));
 #pragma unroll
-          for (int ht = 0; ht < HT; ++ht) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float& x = s[ht][mt][2 * h + c];
-              x *= kCodes ? k_mul * q_mul[ht][c] : q_mul[ht][c];
-              if (!seen) x = -INFINITY;
-              move |= x > m[ht][c] + kSlack;
+            for (int ht = 0; ht < HT; ++ht) {
+              s[ht][mt][2 * h] *= k_mul;
+              s[ht][mt][2 * h + 1] *= k_mul;
             }
           }
+          if (!inside) {
+            bool seen;
+            token_of(tl, tok, seen);
+            if (!seen) {
+              vw[mt][h] = 0.0f;
+#pragma unroll
+              for (int ht = 0; ht < HT; ++ht) s[ht][mt][2 * h] = s[ht][mt][2 * h + 1] = -INFINITY;
+            }
+          }
+        }
+      }
+      if constexpr (kCodes) {
+        float top = fmaxf(vw[0][0], vw[0][1]);
+#pragma unroll
+        for (int mt = 1; mt < MT; ++mt) top = max3(top, vw[mt][0], vw[mt][1]);
+        move = top >= v_limit;
+      }
+#pragma unroll
+      for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = fmaxf(s[ht][0][c], s[ht][0][2 + c]);
+#pragma unroll
+          for (int mt = 1; mt < MT; ++mt) top = max3(top, s[ht][mt][c], s[ht][mt][2 + c]);
+          move |= top * q_mul[ht][c] > m[ht][c] + kSlack;
         }
       }
       // hidden tokens of a group that was copied whole may hold anything: their
       // values have to be finite beside weights of zero (codes always are)
       if constexpr (RUN && !kCodes) {
-        if (__any_sync(0xffffffffu, edge)) {
+        if (!inside) {
           bool seen;
           token_of(tl, lane, seen);
           if (lane < TT && !seen) {
@@ -641,17 +703,18 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       if (__any_sync(0xffffffffu, move)) {
         float v_keep = 1.0f;
         if constexpr (kCodes) {
-          float top = v_top;
+          float top = 0.0f;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(vw[mt][0], vw[mt][1]));
 #pragma unroll
           for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          if (top > v_top) {
+          if (top >= v_limit) {
             const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e) takes top into [1, 2)
             const float next = __uint_as_float((254u - (e < 1u ? 1u : (e > 253u ? 253u : e))) << 23);
-            v_keep = v_top > 0.0f ? next / v_mul : 0.0f;  // nothing but zeros so far: O is 0
-            v_top = top;
+            v_keep = v_first ? 0.0f : next / v_mul;  // nothing but zeros so far: O is 0
+            v_first = false;
             v_mul = next;
+            v_limit = 2.0f / next;
           }
         }
 #pragma unroll
@@ -663,6 +726,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
             for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(s[ht][mt][c], s[ht][mt][2 + c]));
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top *= q_mul[ht][c];
             float keep = 1.0f;
             if (top > m[ht][c]) {
               keep = exp2f(m[ht][c] - top);
@@ -689,7 +753,13 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float w0 = ex2(s[ht][mt][2 * h] - z0), w1 = ex2(s[ht][mt][2 * h + 1] - z1);
+            float w0 = ex2(fmaf(s[ht][mt][2 * h], q_mul[ht][0], -z0)), w1 = ex2(fmaf(s[ht][mt][2 * h + 1], q_mul[ht][1], -z1));
+            if (!inside) {  // a factor of zero takes a hidden token's -infinity to NaN
+              bool seen;
+              token_of(tl, 16 * mt + 8 * h + order, seen);
+              w0 = seen ? w0 : 0.0f;
+              w1 = seen ? w1 : 0.0f;
+            }
             l[ht][0] += w0;
             l[ht][1] += w1;
             if constexpr (kCodes) {
@@ -750,21 +820,15 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       }
       if constexpr (kCodes) {
         // the bias is a sum of weights that an operand of 128s collects; it leaves O
-        // before it grows large beside it
+        // every other tile, before it grows large beside it
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
             mma16816<false>(o_bias[ht], 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, p[ht][mt][0], p[ht][mt][1]);
-#pragma unroll
-          for (int i = 0; i < KS; ++i) {
-            o[ht][i][0] -= o_bias[ht][0];
-            o[ht][i][1] -= o_bias[ht][1];
-            o[ht][i][2] -= o_bias[ht][0];
-            o[ht][i][3] -= o_bias[ht][1];
-          }
-          o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
         }
+        biased = !biased;
+        if (!biased) remove_bias();
       }
       // ---- refill the stage; its table entries were asked for one tile ago
       __syncwarp();
@@ -790,9 +854,9 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       for (int ht = 0; ht < HT; ++ht) l[ht][0] = l[ht][1] = NAN;
     }
 
+    if (kCodes && biased) remove_bias();
     // ---- join the warps
     const float v_undo = (kCodes ? 0x1p24f : 1.0f) / v_mul;
-    __syncthreads();  // every warp is done with its ring
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
@@ -816,11 +880,23 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         }
       }
     }
-    __syncthreads();
-    const bool complete = t0 == 0 && item_begin + n <= tile_end;
-    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (item_begin < range_begin ? 0 : 1)) *
+    // on to the next item: its first copies are on their way while this one is joined
+    const bool complete = t0 == 0 && item_begin + n <= tile_end, empty = vis.len == 0;
+    const int done_head0 = head0, done_heads = heads;
+    const int64_t done_seq = seq, done_begin = item_begin;
+    tile += t1 - t0;
+    if (tile == base + n * items_per_seq) {
+      base = tile;
+      ++seq;
+      len = len_next;
+      len_next = seq + 1 < a.batch ? a.lengths[seq + 1] : 0;
+    }
+    const bool more = tile < tile_end;
+    if (more) open();
+    __syncthreads();  // every warp has left its part
+    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (done_begin < range_begin ? 0 : 1)) *
                                 static_cast<int64_t>(Shape::kPartFloats);
-    for (int x = threadIdx.x; x < heads * (D / 4); x += kPagedThreads) {
+    for (int x = threadIdx.x; x < done_heads * (D / 4); x += kPagedThreads) {
       const int h = x / (D / 4), c = (x - h * (D / 4)) * 4;
       float top = -INFINITY, total = 0.0f;
 #pragma unroll
@@ -838,8 +914,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         sum.w = fmaf(v.w, f, sum.w);
       }
       if (complete) {
-        const int64_t at = seq * a.q_heads + head0 + h;
-        const float r = vis.len == 0 ? 0.0f : 1.0f / total;
+        const int64_t at = done_seq * a.q_heads + done_head0 + h;
+        const float r = empty ? 0.0f : 1.0f / total;
         T* out = static_cast<T*>(a.out) + at * D + c;
         uint2 w;
         if constexpr (__is_same(T, __nv_bfloat16)) {
@@ -849,7 +925,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         }
         *reinterpret_cast<uint2*>(out) = w;
         if (a.lse != nullptr && c == 0)
-          a.lse[at] = vis.len == 0 ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
+          a.lse[at] = empty ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(part + h * D + c) = sum;
         if (c == 0) {
@@ -858,11 +934,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         }
       }
     }
-    tile += t1 - t0;
-    if (tile == base + n * items_per_seq) {  // on to the next sequence
-      base = tile;
-      ++seq;
-    }
+    if (!more) break;
+    __syncthreads();  // the parts are read; the next item's go there
   }
 }
 
