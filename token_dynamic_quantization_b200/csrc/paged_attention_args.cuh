@@ -6,6 +6,13 @@
 
 namespace dq {
 
+// The item inside which a CTA's range of work units ends (seq < 0: it ends with one).
+struct PagedCut {
+  int64_t begin, tiles;  // the item's first unit, and its tiles
+  int64_t seq, item;
+  int64_t per;           // units per CTA
+};
+
 struct PagedArgs {
   const void* q;
   int64_t q_stride;
@@ -27,8 +34,8 @@ struct PagedArgs {
   // tensor-core kernels only
   uint32_t page_mul, page_shift;  // token / page_size = (mulhi(token, mul) + token) >> shift
   int head_sets;                  // sets of 8 * HT query heads that share a key head
-  int64_t items;                  // batch * kv_heads * head_sets
-  float* parts;                   // workspace: what CTAs leave of sequences that they share
+  float* parts;                   // workspace: what CTAs leave of items that they share
+  PagedCut* cuts;                 // workspace, one per CTA
   int whole;                      // 1: a CTA per item, nothing shared
 };
 

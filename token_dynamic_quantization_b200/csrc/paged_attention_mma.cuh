@@ -46,20 +46,16 @@ constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the running 
 constexpr float kLift = 6.0f;   // log2 of the weight at the running maximum
 constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;  // row numbers outside every cache
 
-#ifndef PA_TT8
-#define PA_TT8 32
-#endif
-#ifndef PA_CTAS
-#define PA_CTAS 3
-#endif
 template <typename C, int D, int HT>
 struct PagedShape {
   static constexpr bool kCodes = sizeof(C) == 1;
-  static constexpr int kTokens = kCodes && D <= 128 ? PA_TT8 : 16;
+  static constexpr int kTokens = kCodes && D <= 128 ? 32 : 16;
   static constexpr int kHeads = 8 * HT;
   // one CTA's parts: O [kHeads][D], then (max, sum) [kHeads]
   static constexpr int kPartFloats = kHeads * D + 2 * kHeads;
-  static constexpr int kCtas = HT * D > 128 ? 2 : PA_CTAS;  // CTAs per SM
+  // CTAs per SM: three, and two where their rings would be too short (codes of 128
+  // channels: 109 us with two, 115 with three) or the registers do not allow more
+  static constexpr int kCtas = HT * D > 128 || (kCodes && D == 128) ? 2 : 3;
   // rows lie in shared memory in boxes of 128 bytes (64 for 64 codes), swizzled
   static constexpr int kBox = D * int(sizeof(C)) < 128 ? D * int(sizeof(C)) : 128;
   static constexpr int kBoxes = D * int(sizeof(C)) / kBox;
@@ -67,7 +63,8 @@ struct PagedShape {
   static constexpr int kRowBytes = kTokens * D * int(sizeof(C));
   static constexpr int kScaleBytes = kCodes ? 2 * 4 * kTokens : 0;
   static constexpr int kStageBytes = 2 * kRowBytes;
-  static constexpr int kJoin = kPagedWarps * (kHeads * D + 2 * kHeads) * 4;
+  static constexpr int kPitch = D + 4;                      // of a head's row there, against bank conflicts
+  static constexpr int kJoin = kPagedWarps * (kHeads * kPitch + 2 * kHeads) * 4;
   static constexpr int kFit = (227 * 1024 / kCtas - 2048 - 256 - kJoin) / kPagedWarps / (kStageBytes + kScaleBytes);
   static constexpr int kStages = kFit < 2 ? 2 : (kFit > 8 ? 8 : kFit);
   static constexpr int kRings = kPagedWarps * kStages * kStageBytes;
@@ -225,6 +222,12 @@ __device__ __forceinline__ Groups visible_groups(const PagedArgs& a, int len) {
   return v;
 }
 
+// Opening and joining an item takes a CTA as long as several tiles (3.4 us against
+// 0.6 us a tile on 64 sequences of up to 8192 tokens): ranges are cut in units of
+// which an item has kItemCost more than tiles, the first ones empty. On those
+// sequences, INT8, 137 us with 0, 119 with 4, 115 with 6 and 10.
+constexpr int kItemCost = 8;
+
 // Tiles of one sequence's item; a sequence without tokens still has one, whose
 // CTA writes its zeros.
 template <int TT>
@@ -233,8 +236,8 @@ __device__ __forceinline__ int tiles_of(const Groups& v) {
   return v.count == 0 ? 1 : (v.count + kGroups - 1) / kGroups;
 }
 template <int TT>
-__device__ __forceinline__ int64_t item_tiles(const PagedArgs& a, int64_t b) {
-  return tiles_of<TT>(visible_groups(a, a.lengths[b]));
+__device__ __forceinline__ int64_t item_units(const PagedArgs& a, int64_t b) {
+  return tiles_of<TT>(visible_groups(a, a.lengths[b])) + kItemCost;
 }
 
 __device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
@@ -243,16 +246,16 @@ __device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
   return v;
 }
 
-// All tiles of the call (every lane of the warp gets the sum).
+// All units of the call (every lane of the warp gets the sum).
 template <int TT>
-__device__ int64_t total_tiles(const PagedArgs& a) {
+__device__ int64_t total_units(const PagedArgs& a) {
   int64_t sum = 0;
   const int lane = threadIdx.x & 31;
-  for (int64_t b = lane; b < a.batch; b += 32) sum += item_tiles<TT>(a, b);
+  for (int64_t b = lane; b < a.batch; b += 32) sum += item_units<TT>(a, b);
   return warp_sum_i64(sum) * a.kv_heads * a.head_sets;
 }
 
-// The sequence that tile `x` belongs to, and the number of its first tile.
+// The sequence that unit `x` belongs to, and the number of its first unit.
 template <int TT>
 __device__ void find_sequence(const PagedArgs& a, int64_t x, int64_t& seq, int64_t& base) {
   const int lane = threadIdx.x & 31;
@@ -260,7 +263,7 @@ __device__ void find_sequence(const PagedArgs& a, int64_t x, int64_t& seq, int64
   int64_t before = 0;
   for (int64_t b0 = 0;; b0 += 32) {
     const int64_t b = b0 + lane;
-    int64_t end = b < a.batch ? item_tiles<TT>(a, b) * per : 0;
+    int64_t end = b < a.batch ? item_units<TT>(a, b) * per : 0;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int64_t up = __shfl_up_sync(0xffffffffu, end, o);
@@ -279,10 +282,10 @@ __device__ void find_sequence(const PagedArgs& a, int64_t x, int64_t& seq, int64
   }
 }
 
-// Tiles per CTA: equal shares, and at least one for each warp.
-__device__ __forceinline__ int64_t tiles_per_cta(int64_t total, int64_t ctas) {
+// Units per CTA: equal shares, and at least a short item for each.
+__device__ __forceinline__ int64_t units_per_cta(int64_t total, int64_t ctas) {
   const int64_t per = (total + ctas - 1) / ctas;
-  return per < kPagedWarps ? kPagedWarps : per;
+  return per < kItemCost + kPagedWarps ? kItemCost + kPagedWarps : per;
 }
 
 // ---------------------------------------------------------------- main kernel
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // the warps' rings and scales; what they leave of an item, [warps][kHeads][D] and [warps][kHeads][2]
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRings + Shape::kScales);
-  float* s_stat = s_o + kPagedWarps * kHeads * D;
+  float* s_stat = s_o + kPagedWarps * kHeads * Shape::kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * kStages * Shape::kStageBytes;
@@ -320,49 +323,68 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
   pdl_launch_dependents();
   pdl_wait_primary();
 
-  int64_t seq, base, tile, tile_end;
-  const int64_t items_per_seq = static_cast<int64_t>(a.kv_heads) * a.head_sets;
+  // this CTA's units [unit, unit_end); `base` is the first one of sequence seq
+  int64_t seq, base, unit, unit_end;
+  const int items_per_seq = a.kv_heads * a.head_sets;
   if (a.whole) {
     seq = blockIdx.x / items_per_seq;
-    const int64_t n = item_tiles<TT>(a, seq);
+    const int64_t n = item_units<TT>(a, seq);
     base = 0;
-    tile = (blockIdx.x - seq * items_per_seq) * n;
-    tile_end = tile + n;
+    unit = (blockIdx.x - seq * items_per_seq) * n;
+    unit_end = unit + n;
   } else {
-    const int64_t total = total_tiles<TT>(a);
-    const int64_t per = tiles_per_cta(total, gridDim.x);
-    tile = per * blockIdx.x;
-    tile_end = tile + per < total ? tile + per : total;
-    if (tile >= total) return;
-    find_sequence<TT>(a, tile, seq, base);
+    const int64_t total = total_units<TT>(a);
+    const int64_t per = units_per_cta(total, gridDim.x);
+    unit = per * blockIdx.x;
+    unit_end = unit + per < total ? unit + per : total;
+    if (unit >= total) {
+      if (threadIdx.x == 0) a.cuts[blockIdx.x].seq = -1;
+      return;
+    }
+    find_sequence<TT>(a, unit, seq, base);
   }
-  const int64_t range_begin = tile;
+  const int64_t range_begin = unit;
   // tokens of a tile in the order that spreads them over the banks: lane g's K
   // row, and the rows of a lane's V tokens
   const int order = token_order<Shape::kBox>(g), order_even = token_order<Shape::kBox>(2 * t);
   const int order_odd = token_order<Shape::kBox>(2 * t + 1);
 
 
-  // ---- the item at `tile`: its tokens, heads and rows of the page table
-  Groups vis;
-  int64_t n = 0, item = 0, item_begin = 0;
-  int t0 = 0, t1 = 0, kvh = 0, head0 = 0, heads = 0;
-  const int32_t* table = nullptr;
+  // ---- the item at hand: its tokens, heads and rows of the page table; this CTA
+  // has its tiles [t0, t1)
   int len = a.lengths[seq], len_next = seq + 1 < a.batch ? a.lengths[seq + 1] : 0;
+  Groups vis = visible_groups(a, len);
+  int n = tiles_of<TT>(vis);
+  int item = static_cast<int>((unit - base) / (n + kItemCost));
+  int64_t item_begin = base + static_cast<int64_t>(item) * (n + kItemCost);
+  int kvh = item / a.head_sets, set = item - kvh * a.head_sets;
+  int t0 = 0, t1 = 0, head0 = 0, heads = 0;
+  const int32_t* table = a.page_table + seq * a.max_pages;
   const auto enter = [&]() {
-    vis = visible_groups(a, len);
-    n = tiles_of<TT>(vis);
-    item = (tile - base) / n;
-    item_begin = base + item * n;
-    t0 = static_cast<int>(tile - item_begin);
-    t1 = static_cast<int>((item_begin + n < tile_end ? item_begin + n : tile_end) - item_begin);
-    kvh = static_cast<int>(item / a.head_sets);
-    const int set = static_cast<int>(item - static_cast<int64_t>(kvh) * a.head_sets);
-    head0 = kvh * a.group + set * kHeads;                                  // first query head
+    const int64_t first = unit - item_begin - kItemCost, last = unit_end - item_begin - kItemCost;
+    t0 = first < 0 ? 0 : static_cast<int>(first);
+    t1 = last < n ? static_cast<int>(last) : n;  // <= 0: the range ends in the item's empty units
+    head0 = kvh * a.group + set * kHeads;        // first query head
     heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
-    table = a.page_table + seq * a.max_pages;
   };
-
+  // the item behind the one at hand
+  const auto advance = [&]() {
+    item_begin += n + kItemCost;
+    unit = item_begin;
+    ++item;
+    if (++set == a.head_sets) {
+      set = 0;
+      if (++kvh == a.kv_heads) {
+        kvh = item = 0;
+        ++seq;
+        len = len_next;
+        len_next = seq + 1 < a.batch ? a.lengths[seq + 1] : 0;
+        vis = visible_groups(a, len);
+        n = tiles_of<TT>(vis);
+        table += a.max_pages;
+      }
+    }
+  };
     // Token at place r of tile tl, and whether it is visible.
     const auto token_of = [&](int tl, int r, bool& seen) -> int {
       const int group = tl * MT + (r >> 4);
@@ -478,6 +500,11 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       page_next = find_page(first + kStages * kPagedWarps, in_page_next);
     };
 
+  enter();
+  if (t1 <= t0) {  // the range is nothing but empty units: they end with it, or its item is the next CTA's
+    if (threadIdx.x == 0) a.cuts[blockIdx.x].seq = -1;
+    return;
+  }
   open();
   while (true) {
     // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
@@ -869,32 +896,28 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
           s_stat[(warp * kHeads + h) * 2] = m[ht][c];
           s_stat[(warp * kHeads + h) * 2 + 1] = sum;
         }
-        float* dst = s_o + (warp * kHeads + h) * D;
+        // row tile i holds the lane's channels 2i and 2i + 1, counted over its V pieces
+        float* dst = s_o + (warp * kHeads + h) * Shape::kPitch + kVPiece * g;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          // row tile i holds the lane's channels 2i and 2i + 1, counted over its V pieces
-          const int e = 2 * i;
-          const int ch = (e / kVPiece) * 8 * kVPiece + kVPiece * g + e % kVPiece;
-          dst[ch] = o[ht][i][c] * v_undo;
-          dst[ch + 1] = o[ht][i][2 + c] * v_undo;
+        for (int i = 0; i < KS; i += 2) {
+          const int ch = (2 * i / kVPiece) * 8 * kVPiece + 2 * i % kVPiece;
+          *reinterpret_cast<float4*>(dst + ch) = make_float4(o[ht][i][c] * v_undo, o[ht][i][2 + c] * v_undo,
+                                                             o[ht][i + 1][c] * v_undo, o[ht][i + 1][2 + c] * v_undo);
         }
       }
     }
     // on to the next item: its first copies are on their way while this one is joined
-    const bool complete = t0 == 0 && item_begin + n <= tile_end, empty = vis.len == 0;
+    const bool complete = t0 == 0 && t1 == n, empty = vis.len == 0;
     const int done_head0 = head0, done_heads = heads;
     const int64_t done_seq = seq, done_begin = item_begin;
-    tile += t1 - t0;
-    if (tile == base + n * items_per_seq) {
-      base = tile;
-      ++seq;
-      len = len_next;
-      len_next = seq + 1 < a.batch ? a.lengths[seq + 1] : 0;
-    }
-    const bool more = tile < tile_end;
+    const bool cut = t1 < n;  // the range ends inside the item
+    if (cut && threadIdx.x == 0) a.cuts[blockIdx.x] = {done_begin, n, seq, item, static_cast<int64_t>(unit_end - range_begin)};
+    advance();
+    const bool more = unit + kItemCost < unit_end;  // a tile of it is this CTA's
+    if (!cut && !more && !a.whole && threadIdx.x == 0) a.cuts[blockIdx.x].seq = -1;
     if (more) open();
     __syncthreads();  // every warp has left its part
-    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (done_begin < range_begin ? 0 : 1)) *
+    float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (done_begin + kItemCost < range_begin ? 0 : 1)) *
                                 static_cast<int64_t>(Shape::kPartFloats);
     for (int x = threadIdx.x; x < done_heads * (D / 4); x += kPagedThreads) {
       const int h = x / (D / 4), c = (x - h * (D / 4)) * 4;
@@ -907,7 +930,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         const float mw = s_stat[(w * kHeads + h) * 2];
         const float f = mw == top ? 1.0f : exp2f(mw - top);
         total = fmaf(s_stat[(w * kHeads + h) * 2 + 1], f, total);
-        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * D + c);
+        const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * Shape::kPitch + c);
         sum.x = fmaf(v.x, f, sum.x);
         sum.y = fmaf(v.y, f, sum.y);
         sum.z = fmaf(v.z, f, sum.z);
@@ -941,50 +964,33 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
 
 // ---------------------------------------------------------------- joining kernel
 
-// Joins what CTAs have left of an item that their ranges cut. By item where
-// there are fewer items than CTAs, else one CTA per border between ranges (the
-// first border inside an item takes it); the heads spread over grid.y.
+constexpr int kPagedJoinThreads = 512;
+
+// Joins what CTAs have left of the items that their ranges cut: one CTA per
+// border between two ranges; the first border inside an item takes it. A head
+// takes D / 4 threads, and what threads are left share its parts.
 template <typename T, typename C, int D, int HT>
-__global__ void __launch_bounds__(kPagedThreads) paged_attention_join_kernel(const PagedArgs a, const int ctas,
-                                                                             const int by_item) {
+__global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel(const PagedArgs a) {
   using Shape = PagedShape<C, D, HT>;
-  constexpr int TT = Shape::kTokens, kHeads = Shape::kHeads;
-  constexpr int kVec = D / 4, kSplit = kPagedThreads / kVec < 1 ? 1 : kPagedThreads / kVec;
-  __shared__ float s_o[kSplit][D];
-  __shared__ float s_m[kSplit], s_l[kSplit];
+  constexpr int kHeads = Shape::kHeads, kVec = D / 4, kRows = kPagedJoinThreads / kVec;
+  __shared__ float s_o[kRows][D];
+  __shared__ float s_m[kRows], s_l[kRows];
   pdl_launch_dependents();
   pdl_wait_primary();
-  const int64_t items_per_seq = static_cast<int64_t>(a.kv_heads) * a.head_sets;
-  const int64_t total = total_tiles<TT>(a);
-  const int64_t per = tiles_per_cta(total, ctas);
-  int64_t seq, base, item, n;
-  if (by_item) {
-    seq = blockIdx.x / items_per_seq;
-    item = blockIdx.x - seq * items_per_seq;
-    n = item_tiles<TT>(a, seq);
-    int64_t sum = 0;
-    for (int64_t b = threadIdx.x & 31; b < seq; b += 32) sum += item_tiles<TT>(a, b);
-    base = warp_sum_i64(sum) * items_per_seq;
-  } else {
-    const int64_t x = per * (static_cast<int64_t>(blockIdx.x) + 1);
-    if (x >= total) return;
-    find_sequence<TT>(a, x, seq, base);
-    n = item_tiles<TT>(a, seq);
-    item = (x - base) / n;
-  }
-  const int64_t begin = base + item * n;
-  const int64_t c0 = begin / per, c1 = (begin + n - 1) / per;
-  if (c0 == c1 || (!by_item && c0 != static_cast<int64_t>(blockIdx.x))) return;
-  const int kvh = static_cast<int>(item / a.head_sets);
-  const int set = static_cast<int>(item - static_cast<int64_t>(kvh) * a.head_sets);
+  const PagedCut cut = a.cuts[blockIdx.x];
+  if (cut.seq < 0) return;
+  const int64_t c0 = (cut.begin + kItemCost) / cut.per, c1 = (cut.begin + kItemCost + cut.tiles - 1) / cut.per;
+  if (c0 != static_cast<int64_t>(blockIdx.x)) return;
+  const int kvh = static_cast<int>(cut.item) / a.head_sets, set = static_cast<int>(cut.item) - kvh * a.head_sets;
   const int heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
-  const int vec = threadIdx.x % kVec, split = threadIdx.x / kVec;
+  const int vec = threadIdx.x % kVec, row = threadIdx.x / kVec;
+  const int splits = kRows / heads, h = row % heads, split = row / heads;  // kRows >= kHeads
 
-  for (int h = blockIdx.y; h < heads; h += gridDim.y) {
-    float top = -INFINITY, sum_l = 0.0f;
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int64_t c = c0 + split; c <= c1; c += kSplit) {
+  float top = -INFINITY, sum_l = 0.0f;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (split < splits) {
+#pragma unroll 8
+    for (int64_t c = c0 + split; c <= c1; c += splits) {
       const float* part = a.parts + (c * 2 + (c == c0 ? 1 : 0)) * static_cast<int64_t>(Shape::kPartFloats);
       const float2 st = *reinterpret_cast<const float2*>(part + kHeads * D + 2 * h);
       const float4 v = *reinterpret_cast<const float4*>(part + h * D + 4 * vec);
@@ -997,30 +1003,25 @@ __global__ void __launch_bounds__(kPagedThreads) paged_attention_join_kernel(con
       sum.w = fmaf(v.w, f, sum.w * keep);
       top = next;
     }
-    __syncthreads();  // the previous head's readers are done
-    *reinterpret_cast<float4*>(&s_o[split][4 * vec]) = sum;
-    if (vec == 0) {
-      s_m[split] = top;
-      s_l[split] = sum_l;
+  }
+  *reinterpret_cast<float4*>(&s_o[row][4 * vec]) = sum;
+  if (vec == 0) {
+    s_m[row] = top;
+    s_l[row] = sum_l;
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < heads * D; x += kPagedJoinThreads) {
+    const int hx = x / D, c = x - hx * D;
+    float all = -INFINITY, total = 0.0f, r = 0.0f;
+    for (int p = hx; p < splits * heads; p += heads) all = fmaxf(all, s_m[p]);
+    for (int p = hx; p < splits * heads; p += heads) {
+      const float f = s_m[p] == all ? 1.0f : exp2f(s_m[p] - all);
+      total = fmaf(s_l[p], f, total);
+      r = fmaf(s_o[p][c], f, r);
     }
-    __syncthreads();
-    const int64_t at = seq * a.q_heads + kvh * a.group + set * kHeads + h;
-    float all = -INFINITY, total_l = 0.0f, f[kSplit];
-#pragma unroll
-    for (int p = 0; p < kSplit; ++p) all = fmaxf(all, s_m[p]);
-#pragma unroll
-    for (int p = 0; p < kSplit; ++p) {
-      f[p] = s_m[p] == all ? 1.0f : exp2f(s_m[p] - all);
-      total_l = fmaf(s_l[p], f[p], total_l);
-    }
-    for (int c = threadIdx.x; c < D; c += kPagedThreads) {
-      float r = 0.0f;
-#pragma unroll
-      for (int p = 0; p < kSplit; ++p) r = fmaf(s_o[p][c], f[p], r);
-      static_cast<T*>(a.out)[at * D + c] = static_cast<T>(r / total_l);
-    }
-    if (threadIdx.x == 0 && a.lse != nullptr)
-      a.lse[at] = ((all == -INFINITY ? 0.0f : all) - kLift + log2f(total_l)) * kLn2;
+    const int64_t at = cut.seq * a.q_heads + kvh * a.group + set * kHeads + hx;
+    static_cast<T*>(a.out)[at * D + c] = static_cast<T>(r / total);
+    if (c == 0 && a.lse != nullptr) a.lse[at] = ((all == -INFINITY ? 0.0f : all) - kLift + log2f(total)) * kLn2;
   }
 }
 

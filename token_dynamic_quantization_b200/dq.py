@@ -15,6 +15,7 @@ missing; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdq.so")
@@ -271,7 +272,7 @@ def dynamic_quant(x, smooth=None, group_index=None, mode: str = "symmetric", y_d
     else:
         y, scale, offset, ws = out
     if stream is None:
-        stream = torch.cuda.current_stream(x.device).cuda_stream
+        stream = _stream_of(x.get_device())
     st = dq_dynamic_quant(_dev_ptr(x, "x"), _dtype_code(x), rows, cols,
                           _dev_ptr(smooth, "smooth"), _dtype_code(smooth) if smooth is not None else DQ_F32,
                           _dev_ptr(group_index, "group_index"), ngroups, m, yc,
@@ -307,7 +308,7 @@ def ada_layernorm_quant(x, ada_scale, ada_shift, weight=None, bias=None, smooth=
     if workspace is None and ws_bytes:
         workspace = torch.empty((ws_bytes + 15) // 16 * 4, dtype=torch.float32, device=x.device)
     if stream is None:
-        stream = torch.cuda.current_stream(x.device).cuda_stream
+        stream = _stream_of(x.get_device())
     st = dq_ada_layernorm_quant(_dev_ptr(x, "x"), _dtype_code(x), batch, seq, hidden,
                                 _dev_ptr(ada_scale, "ada_scale"), _dev_ptr(ada_shift, "ada_shift"),
                                 _dev_ptr(weight, "weight"), _dev_ptr(bias, "bias"), _dev_ptr(smooth, "smooth"),
@@ -341,7 +342,7 @@ def dequant_per_token(y, scale, offset=None, y_dtype: str = "int8", cols: int | 
     if out is None:
         out = torch.empty((rows, cols), dtype=out_dtype, device=y.device)
     if stream is None:
-        stream = torch.cuda.current_stream(y.device).cuda_stream
+        stream = _stream_of(y.get_device())
     st = dq_dequant_per_token(_dev_ptr(y, "y"), yc, rows, cols, _dev_ptr(scale, "scale"), _dev_ptr(offset, "offset"),
                               sdt, _dev_ptr(out, "out"), _dtype_code(out), stream)
     if check and st != DQ_OK:
@@ -368,7 +369,7 @@ def dequant_per_group(y, scale, offset=None, group_size: int = 32, k_dim: int = 
     if out is None:
         out = torch.empty((rows, cols), dtype=out_dtype or scale.dtype, device=y.device)
     if stream is None:
-        stream = torch.cuda.current_stream(y.device).cuda_stream
+        stream = _stream_of(y.get_device())
     st = dq_dequant_per_group(_dev_ptr(y, "y"), yc, rows, cols, _dev_ptr(scale, "scale"), _dev_ptr(offset, "offset"),
                               sdt, int(group_size), int(k_dim), _dev_ptr(out, "out"), _dtype_code(out), stream)
     if check and st != DQ_OK:
@@ -398,7 +399,7 @@ def w8a8_gemm(a, b, a_scale, b_scale, out_dtype=None, out=None, accumulate: bool
     elif tuple(out.shape) != (m, n):
         raise ValueError(f"out must be [{m}, {n}], got {tuple(out.shape)}")
     if stream is None:
-        stream = torch.cuda.current_stream(a.device).cuda_stream
+        stream = _stream_of(a.get_device())
     st = dq_w8a8_gemm(_dev_ptr(a, "a"), _dev_ptr(b, "b"), m, n, k, _dev_ptr(a_scale, "a_scale"),
                       _dev_ptr(b_scale, "b_scale"), _dev_ptr(out, "out"), _dtype_code(out), 1 if accumulate else 0,
                       stream)
@@ -625,6 +626,12 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_
     return out
 
 
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes(index: int, q_heads: int, kv_heads: int, dim: int, cache_dtype: int) -> int:
+    """dq_paged_attention's workspace on device `index`, the current one; the batch does not matter."""
+    return dq_paged_attention_get_workspace_size(1, q_heads, kv_heads, dim, cache_dtype)
+
+
 def paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale=None, v_scale=None, softmax_scale=None,
                     window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None,
                     check: bool = True):
@@ -654,7 +661,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale=None, v_sc
         out = q.new_empty(shape)
     kc, vc, cdt, ks, vs, pages, page_size = _cache_args(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, index)
     if workspace is None:
-        ws_bytes = dq_paged_attention_get_workspace_size(batch, q_heads, kv_heads, dim, cdt)
+        ws_bytes = _workspace_bytes(index, q_heads, kv_heads, dim, cdt)
         if ws_bytes:
             workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
     elif workspace.get_device() != index or not workspace.is_contiguous():
