@@ -22,6 +22,7 @@ struct LinearArgs {
   int bias_dtype;
   int out_kind;  // kOutF32 / kOutF16 / kOutBF16
   int vec_out;   // rows of out (and residual) start 16-byte aligned
+  int pair_out;  // two neighbouring even columns lie in one aligned access, in every row
 };
 
 __device__ __forceinline__ float exp2_approx(float x) {

@@ -1,7 +1,6 @@
 // W8A8 product with bias, activation and residual in its epilogue
 // (dq_w8a8_linear).
 #include <atomic>
-#include <cstdio>
 
 #include "dq.h"
 #include "dq_launch.cuh"
@@ -35,16 +34,6 @@ __global__ void __launch_bounds__(256) w8a8_linear_generic_kernel(const LinearAr
 }
 
 }  // namespace dq
-
-#ifndef DQ_SPLIT_MOST
-#define DQ_SPLIT_MOST 256
-#endif
-#ifndef FEW_SPLIT
-#define FEW_SPLIT 1
-#endif
-#ifndef DQ_FEW
-#define DQ_FEW 8
-#endif
 
 namespace {
 
@@ -92,21 +81,6 @@ const int* resident_clusters(Kernel kernel, int device, int block, size_t smem, 
   return out;
 }
 
-// The same for CTAs of which several share an SM: the split whose busiest SM has
-// the least to read, and of equal ones the largest (more loads in flight).
-int even_split(int64_t tiles, int64_t pieces, int64_t sms) {
-  int split = 1;
-  double best = 0.0;
-  for (int s = 1; s <= kMaxSplit && s <= pieces; ++s) {
-    const double time = static_cast<double>((tiles * s + sms - 1) / sms) * static_cast<double>((pieces + s - 1) / s);
-    if (s == 1 || time <= 1.02 * best) {
-      best = s == 1 || time < best ? time : best;
-      split = s;
-    }
-  }
-  return split;
-}
-
 // CTAs of a cluster among which K is split: the number whose clusters take the
 // least time, in waves of resident clusters with K / split each; a larger one
 // has to gain 5 %.
@@ -148,22 +122,17 @@ dq_status launch_cluster(Kernel kernel, dim3 grid, int block, size_t smem, int c
   return dq_host::launch_status();
 }
 
-// Few tokens: row blocks of 16 * (8 / KW) weight rows, K split over the CTAs of
-// a cluster.
-template <int ACT, int NT, int RS, int KW>
+// Up to 8 tokens: a CTA for every 16 weight rows.
+template <int ACT>
 dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
-  using Shape = dq::FewShape<NT, RS, KW>;
-  auto fn = dq::w8a8_linear_few_kernel<ACT, NT, RS, KW>;
-  const int device = dq_host::current_device();
-  if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
-  const int64_t blocks = (a.n + Shape::kRows - 1) / Shape::kRows, token_blocks = (a.m + Shape::kTokens - 1) / Shape::kTokens;
-  const int64_t chunks = (a.k + Shape::kChunk - 1) / Shape::kChunk;
-  const int split = FEW_SPLIT ? FEW_SPLIT : even_split(blocks * token_blocks, chunks, dq_host::sm_count(device));
-  return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
-                        dq::kFewThreads, Shape::kSmem, split, stream, a, split);
+  void (*fn)(const dq::LinearArgs) = dq::w8a8_linear_few_kernel<ACT>;
+  if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), dq_host::current_device(), dq::kFewSmem))
+    return dq_host::kNotLaunchable;
+  return dq_host::launch_programmatic(fn, a, static_cast<int>((a.n + dq::kFewRows - 1) / dq::kFewRows), dq::kFewThreads,
+                                      dq::kFewSmem, stream);
 }
 
-// Up to a few hundred tokens: tiles of 128 weight rows by TOK tokens, K split
+// 9 to 128 tokens: tiles of 128 weight rows by TOK tokens, K split
 // over the CTAs of a cluster.
 template <int ACT, int TOK>
 dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
@@ -180,24 +149,19 @@ dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
   if (device < 0 || device >= dq_host::kMaxDevices) return dq_host::kNotLaunchable;
   const int split = best_split(blocks * token_blocks, (a.k + 127) / 128,
                                resident_clusters(fn, device, dq::kSplitThreads, Shape::kSmem, known[device], resident));
-#ifdef DQ_DEBUG_SPLIT
-  printf("split %d of tiles %ld resident", split, (long)(blocks * token_blocks));
-  for (int s = 1; s <= kMaxSplit; ++s) printf(" %d", resident[s]);
-  printf("\n");
-#endif
   return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
                         dq::kSplitThreads, Shape::kSmem, split, stream, w, x, a, split);
 }
 
 // Many tokens: one pair of CTAs for every two SMs over the list of tiles.
-template <int ACT>
+template <int ACT, bool TURN>
 dq_status launch_pair(const dq::LinearArgs& a, cudaStream_t stream) {
-  auto fn = dq::w8a8_linear_pair_kernel<ACT>;
+  auto fn = dq::w8a8_linear_pair_kernel<ACT, TURN>;
   const int device = dq_host::current_device();
   CUtensorMap ma, mb128, mb64;
   if (!dq_host::make_map(&ma, a.a, a.m, a.k, 128) || !dq_host::make_map(&mb128, a.b, a.n, a.k, 128) ||
       !dq_host::make_map(&mb64, a.b, a.n, a.k, 64) ||
-      !dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, dq::kPairSmem))
+      !dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, dq::PairShape<TURN>::kSmem))
     return dq_host::kNotLaunchable;
   const int64_t pairs = dq_host::sm_count(device) / 2;
   dq::PairSched ps;
@@ -207,7 +171,7 @@ dq_status launch_pair(const dq::LinearArgs& a, cudaStream_t stream) {
   ps.wide = tiles - split;
   ps.items = tiles + split;
   const int64_t clusters = ps.items < pairs ? ps.items : pairs;
-  return launch_cluster(fn, dim3(static_cast<unsigned>(2 * clusters)), dq::kPairThreads, dq::kPairSmem, 1, stream, ma,
+  return launch_cluster(fn, dim3(static_cast<unsigned>(2 * clusters)), dq::kPairThreads, dq::PairShape<TURN>::kSmem, 1, stream, ma,
                         mb128, mb64, a, ps);
 }
 
@@ -215,14 +179,14 @@ template <int ACT>
 dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
   // 16-byte pieces of K
   const bool pieces = a.k % 16 == 0 && aligned(a.a, 16) && aligned(a.b, 16);
-  if (pieces && a.n <= int64_t(1) << 28 && (a.m + 63) / 64 <= 65535) {
-    dq_status st = dq_host::kNotLaunchable;
-    if (a.m <= DQ_FEW) {
-      st = a.m <= 8    ? launch_few<ACT, 1, 1, 4>(a, stream)
-           : a.m <= 16 ? launch_few<ACT, 2, 1, 4>(a, stream)
-           : a.m <= 32 ? launch_few<ACT, 4, FEW_RS2, FEW_KW2>(a, stream)
-           : a.m <= 48 ? launch_few<ACT, 6, FEW_RS2, FEW_KW2>(a, stream)
-                       : launch_few<ACT, 8, FEW_RS2, FEW_KW2>(a, stream);
+  if (pieces) {
+    // By the number of tokens, measured at n = k = 4096 to bf16 with bias and
+    // residual: 8 tokens take 6.2 us with the first kernel and 8.2 with the second; 16
+    // take 9.0 with the second and 10.6 with the first; 128 take 16.4 with the second
+    // and 17.4 with the third, 200 19.3 and 17.6.
+    dq_status st;
+    if (a.m <= dq::kFewTokens) {
+      st = launch_few<ACT>(a, stream);
     } else if (a.m <= 16) {
       st = launch_split<ACT, 16>(a, stream);
     } else if (a.m <= 32) {
@@ -231,10 +195,8 @@ dq_status dispatch(const dq::LinearArgs& a, cudaStream_t stream) {
       st = launch_split<ACT, 64>(a, stream);
     } else if (a.m <= 128) {
       st = launch_split<ACT, 128>(a, stream);
-    } else if (a.m <= DQ_SPLIT_MOST) {
-      st = launch_split<ACT, 256>(a, stream);
     } else {
-      st = launch_pair<ACT>(a, stream);
+      st = a.vec_out && a.n % 32 == 0 ? launch_pair<ACT, false>(a, stream) : launch_pair<ACT, true>(a, stream);
     }
     if (st != dq_host::kNotLaunchable) return st;
   }
@@ -275,6 +237,7 @@ extern "C" dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m,
   args.out_kind = out_dtype == DQ_F32 ? dq::kOutF32 : (out_dtype == DQ_F16 ? dq::kOutF16 : dq::kOutBF16);
   args.vec_out = aligned(out, 16) && (residual == nullptr || aligned(residual, 16)) &&
                  (n * static_cast<int64_t>(os)) % 16 == 0;
+  args.pair_out = n % 2 == 0 && aligned(out, 2 * os) && (residual == nullptr || aligned(residual, 2 * os));
   switch (activation) {
     case DQ_ACT_RELU: return dispatch<DQ_ACT_RELU>(args, stream);
     case DQ_ACT_GELU: return dispatch<DQ_ACT_GELU>(args, stream);

@@ -22,19 +22,31 @@
 #include "dq_launch.cuh"
 #include "tcgen05_i8.cuh"
 #include "w8a8_epilogue.cuh"
-#include "w8a8_linear_few.cuh"
 
 namespace dq {
 
 constexpr int kPairEpilogueWarps = 8;
 constexpr int kPairThreads = 64 + 32 * kPairEpilogueWarps;
-constexpr int kPairStages = 6;
+constexpr int kPairMostStages = 6;
 constexpr uint32_t kPairA = 128 * 128, kPairB = 128 * 128;  // bytes of a stage in one CTA
 constexpr uint32_t kPairStage = kPairA + kPairB;
 constexpr uint32_t kPairCols = 512;
 constexpr uint32_t kPairIdescWide = i8_idesc(256, 256), kPairIdescNarrow = i8_idesc(128, 256);
-// ring, two buffers of 256 column scales and biases, barriers
-constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + 2 * 2 * 256 * 4 + 256;
+// Two epilogues. Where rows of the output (and residual) lie in 16-byte pieces and
+// n is a multiple of 32, a lane finishes its own row, 32 columns at a time.
+// Elsewhere (n odd, unaligned rows) each warp first turns 32 x 32 accumulator words in shared memory, at the
+// price of one stage of the ring, and works along the rows: 1000 x 2051 x 1040 to
+// binary32 takes 12.3 us that way and 17.5 with a row per lane, whose 4-byte stores
+// scatter; but 4096^3 with everything takes 88 us against 67, for the extra
+// instructions.
+constexpr int kPairPitch = 34;
+constexpr uint32_t kPairTurn = kPairEpilogueWarps * 32 * (kPairPitch + 1) * 4;  // the words, and the rows' scales
+template <bool TURN>
+struct PairShape {
+  static constexpr int kStages = TURN ? 5 : kPairMostStages;
+  // ring, two buffers of 256 column scales and biases, the turned words, barriers
+  static constexpr size_t kSmem = 1024 + kStages * kPairStage + 2 * 2 * 256 * 4 + (TURN ? kPairTurn : 0) + 256;
+};
 
 struct PairSched {
   int64_t n_tiles;  // 256-wide column tiles
@@ -83,10 +95,10 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   return r;
 }
 
-// 32 columns of one output row from the accumulator's words.
+// 32 columns of one output row from the accumulator's words, 16-byte rows.
 template <int ACT>
 __device__ __forceinline__ void finish_row32(const LinearArgs& a, int64_t row, int64_t c0, const uint32_t (&r)[32],
-                                             const uint4 (&raw)[4], float sa, const float* scale, const float* bias, bool vec) {
+                                             const uint4 (&raw)[4], float sa, const float* scale, const float* bias) {
   const bool has_bias = a.bias != nullptr;
   const int64_t e = row * a.n + c0;
   const bool narrow = a.out_kind != kOutF32;
@@ -103,15 +115,7 @@ __device__ __forceinline__ void finish_row32(const LinearArgs& a, int64_t row, i
       hi = __fadd2_rn(hi, make_float2(bb.z, bb.w));
     }
     float x[4] = {activate<ACT>(lo.x), activate<ACT>(lo.y), activate<ACT>(hi.x), activate<ACT>(hi.y)};
-    if (!vec) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (c0 + 4 * q + i < a.n) {
-          if (a.residual != nullptr) x[i] = __fadd_rn(x[i], load_out(a.residual, a.out_kind, e + 4 * q + i));
-          store_one(a.out, a.out_kind, e + 4 * q + i, x[i]);
-        }
-      }
-    } else if (narrow) {
+    if (narrow) {
       if (a.residual != nullptr) {
         const uint4 w = raw[q / 2];
         const float2 r0 = unpack2(q & 1 ? w.z : w.x, a.out_kind), r1 = unpack2(q & 1 ? w.w : w.y, a.out_kind);
@@ -130,15 +134,117 @@ __device__ __forceinline__ void finish_row32(const LinearArgs& a, int64_t row, i
   }
 }
 
+// The two neighbouring columns of a lane in 16 rows of a chunk (rows 2i + lane / 16,
+// columns 2 (lane % 16) and the next), as words of the residual.
+struct PairResidual {
+  uint32_t w[32];
+};
+
+// Where the lane's first element lies, how far its rows are apart, and what of it exists.
+struct PairSpan {
+  int64_t e;      // element of row lane / 16
+  int rows;       // of the 16, how many lie before the end of out
+  int columns;    // 0, 1 or 2
+  bool paired;    // both columns in one access
+};
+
+__device__ __forceinline__ PairSpan pair_span(const LinearArgs& a, int64_t row0, int64_t c0, int lane) {
+  PairSpan x;
+  const int64_t row = row0 + (lane >> 4), col = c0 + 2 * (lane & 15);
+  x.e = row * a.n + col;
+  const int64_t left = a.m - row;
+  x.rows = left <= 0 ? 0 : (left >= 32 ? 16 : static_cast<int>((left + 1) / 2));
+  x.columns = col >= a.n ? 0 : (col + 2 <= a.n ? 2 : 1);
+  x.paired = x.columns == 2 && a.pair_out;
+  return x;
+}
+
+__device__ __forceinline__ void ask_residual(const LinearArgs& a, const PairSpan& x, PairResidual& r) {
+  if (a.residual == nullptr || x.columns == 0) return;
+  const int64_t step = 2 * a.n;
+  if (a.out_kind == kOutF32) {
+    const uint32_t* p = static_cast<const uint32_t*>(a.residual) + x.e;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, p += step) {
+      if (i < x.rows) {
+        if (x.paired) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          r.w[2 * i] = v.x;
+          r.w[2 * i + 1] = v.y;
+        } else {
+          r.w[2 * i] = p[0];
+          r.w[2 * i + 1] = x.columns == 2 ? p[1] : 0u;
+        }
+      }
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.residual) + x.e;
+#pragma unroll
+    for (int i = 0; i < 16; ++i, p += step) {
+      if (i < x.rows) {
+        if (x.paired) {
+          r.w[i] = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+          r.w[i] = p[0] | (x.columns == 2 ? static_cast<uint32_t>(p[1]) << 16 : 0u);
+        }
+      }
+    }
+  }
+}
+
+// The lane's 16 x 2 outputs of a chunk whose words lie in `turn`, rows' scales behind them.
 template <int ACT>
+__device__ __forceinline__ void finish_chunk(const LinearArgs& a, const PairSpan& x, const PairResidual& r, const int* turn,
+                                             float2 scale, float2 bias, int lane) {
+  if (x.columns == 0) return;
+  const float* row_scale = reinterpret_cast<const float*>(turn + 32 * kPairPitch);
+  const bool has_bias = a.bias != nullptr, has_residual = a.residual != nullptr;
+  int64_t e = x.e;
+#pragma unroll
+  for (int i = 0; i < 16; ++i, e += 2 * a.n) {
+    const int row = 2 * i + (lane >> 4);
+    const int2 acc = *reinterpret_cast<const int2*>(turn + row * kPairPitch + 2 * (lane & 15));
+    float2 v = __fmul2_rn(make_float2(__int2float_rn(acc.x), __int2float_rn(acc.y)), __fmul2_rn(f2(row_scale[row]), scale));
+    if (has_bias) v = __fadd2_rn(v, bias);
+    v = make_float2(activate<ACT>(v.x), activate<ACT>(v.y));
+    if (a.out_kind == kOutF32) {
+      if (has_residual) v = __fadd2_rn(v, make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1])));
+      if (i < x.rows) {
+        float* o = static_cast<float*>(a.out) + e;
+        if (x.paired) {
+          *reinterpret_cast<float2*>(o) = v;
+        } else {
+          o[0] = v.x;
+          if (x.columns == 2) o[1] = v.y;
+        }
+      }
+    } else {
+      if (has_residual) v = __fadd2_rn(v, unpack2(r.w[i], a.out_kind));
+      const uint32_t w = pack2(v.x, v.y, a.out_kind);
+      if (i < x.rows) {
+        uint16_t* o = static_cast<uint16_t*>(a.out) + e;
+        if (x.paired) {
+          *reinterpret_cast<uint32_t*>(o) = w;
+        } else {
+          o[0] = static_cast<uint16_t>(w);
+          if (x.columns == 2) o[1] = static_cast<uint16_t>(w >> 16);
+        }
+      }
+    }
+  }
+}
+
+template <int ACT, bool TURN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     w8a8_linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b128,
                             const __grid_constant__ CUtensorMap map_b64, const LinearArgs a, const PairSched ps) {
+  constexpr int kPairStages = PairShape<TURN>::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* col_scale = reinterpret_cast<float*>(smem + kPairStages * kPairStage);  // [2][256]
   float* col_bias = col_scale + 2 * 256;                                         // [2][256]
-  uint64_t* full = reinterpret_cast<uint64_t*>(col_bias + 2 * 256);              // the leader's are used
+  int* turns = reinterpret_cast<int*>(col_bias + 2 * 256);                       // [warps][32 * (kPairPitch + 1)]
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(turns) + (TURN ? kPairTurn : 0));  // the leader's are used
   uint64_t* empty = full + kPairStages;
   uint64_t* acc_full = empty + kPairStages;  // [2]
   uint64_t* acc_empty = acc_full + 2;        // [2], the leader's are used
@@ -269,41 +375,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         scale[j] = in ? a.b_scale[n0 + j] : 0.0f;
         bias[j] = in && a.bias != nullptr ? load_param(a.bias, a.bias_dtype, n0 + j) : 0.0f;
       }
-      const int64_t row = m0 + 128 * rank + 32 * quarter + lane;
-      const bool row_ok = row < a.m;
-      const float sa = row_ok ? a.a_scale[row] : 0.0f;
-      // the residual of a chunk is asked for one chunk ahead, the first before the wait
-      const auto ask = [&](int c, uint4(&raw)[4]) {
-        const int64_t c0 = n0 + 32 * c;
-        if (a.residual != nullptr && a.out_kind != kOutF32 && row_ok && a.vec_out && c0 + 32 <= a.n && c < (half + 1) * (bn / 64)) {
-          const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.n + c0);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) raw[q] = p[q];
-        }
-      };
-      uint4 next[4];
-      ask(half * (bn / 64), next);
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpilogueWarps) : "memory");
-      if (!dead) dead = !wait_or_abort_for(acc_full + acc, (i >> 1) & 1, abort_flag, kWaitLimitNs);
-      dead = __any_sync(0xffffffffu, dead);  // the warp agrees: the TMEM loads below are collective
-      tc_fence_after();
-      for (int c = half * (bn / 64); c < (half + 1) * (bn / 64); ++c) {
-        const int64_t c0 = n0 + 32 * c;
-        if (c0 >= a.n) break;  // the same for every lane
-        const bool vec = a.vec_out && c0 + 32 <= a.n;
-        if (dead) {
-          if (row_ok) {
-            for (int j = 0; j < 32 && c0 + j < a.n; ++j) store_one(a.out, a.out_kind, row * a.n + c0 + j, __int_as_float(0x7fc00000));
+      if constexpr (TURN) {
+        const int64_t row0 = m0 + 128 * rank + 32 * quarter;  // the warp's rows
+        int* turn = turns + ew * 32 * (kPairPitch + 1);
+        __syncwarp();  // the previous tile's row scales are read
+        turn[32 * kPairPitch + lane] = __float_as_int(row0 + lane < a.m ? a.a_scale[row0 + lane] : 0.0f);
+        // the residual of a chunk is asked for one chunk ahead, the first before the wait
+        const int c_end = (half + 1) * (bn / 64);
+        PairResidual next;
+        ask_residual(a, pair_span(a, row0, n0 + 32 * half * (bn / 64), lane), next);
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpilogueWarps) : "memory");
+        if (!dead) dead = !wait_or_abort_for(acc_full + acc, (i >> 1) & 1, abort_flag, kWaitLimitNs);
+        dead = __any_sync(0xffffffffu, dead);  // the warp agrees: the TMEM loads below are collective
+        tc_fence_after();
+        for (int c = half * (bn / 64); c < c_end; ++c) {
+          const int64_t c0 = n0 + 32 * c;
+          if (c0 >= a.n) break;  // the same for every lane
+          const PairSpan span = pair_span(a, row0, c0, lane);
+          if (dead) {
+            for (int y = 0; y < span.rows; ++y) {
+              for (int z = 0; z < span.columns; ++z) store_one(a.out, a.out_kind, span.e + 2 * y * a.n + z, __int_as_float(0x7fc00000));
+            }
+            continue;
           }
-          continue;
+          const PairResidual now = next;
+          if (c + 1 < c_end) ask_residual(a, pair_span(a, row0, c0 + 32, lane), next);
+          uint32_t r[32];
+          tc_ld_32cols(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(acc * 256 + 32 * c), r);
+          __syncwarp();  // the previous chunk's words are read
+  #pragma unroll
+          for (int q = 0; q < 16; ++q)
+            *reinterpret_cast<int2*>(turn + lane * kPairPitch + 2 * q) = make_int2(static_cast<int>(r[2 * q]), static_cast<int>(r[2 * q + 1]));
+          __syncwarp();
+          const int col = 32 * c + 2 * (lane & 15);
+          finish_chunk<ACT>(a, span, now, turn, *reinterpret_cast<const float2*>(scale + col), *reinterpret_cast<const float2*>(bias + col), lane);
         }
-        uint4 raw[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) raw[q] = next[q];
-        ask(c + 1, next);
-        uint32_t r[32];
-        tc_ld_32cols(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(acc * 256 + 32 * c), r);
-        if (row_ok) finish_row32<ACT>(a, row, c0, r, raw, sa, scale + 32 * c, bias + 32 * c, vec);
+      } else {
+        const int64_t row = m0 + 128 * rank + 32 * quarter + lane;
+        const bool row_ok = row < a.m;
+        const float sa = row_ok ? a.a_scale[row] : 0.0f;
+        // the residual of a chunk is asked for one chunk ahead, the first before the wait
+        const auto ask = [&](int c, uint4(&raw)[4]) {
+          const int64_t c0 = n0 + 32 * c;
+          if (a.residual != nullptr && a.out_kind != kOutF32 && row_ok && c0 < a.n && c < (half + 1) * (bn / 64)) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + row * a.n + c0);
+  #pragma unroll
+            for (int q = 0; q < 4; ++q) raw[q] = p[q];
+          }
+        };
+        uint4 next[4];
+        ask(half * (bn / 64), next);
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kPairEpilogueWarps) : "memory");
+        if (!dead) dead = !wait_or_abort_for(acc_full + acc, (i >> 1) & 1, abort_flag, kWaitLimitNs);
+        dead = __any_sync(0xffffffffu, dead);  // the warp agrees: the TMEM loads below are collective
+        tc_fence_after();
+        for (int c = half * (bn / 64); c < (half + 1) * (bn / 64); ++c) {
+          const int64_t c0 = n0 + 32 * c;
+          if (c0 >= a.n) break;  // the same for every lane
+          if (dead) {
+            if (row_ok) {
+              for (int j = 0; j < 32 && c0 + j < a.n; ++j) store_one(a.out, a.out_kind, row * a.n + c0 + j, __int_as_float(0x7fc00000));
+            }
+            continue;
+          }
+          uint4 raw[4];
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) raw[q] = next[q];
+          ask(c + 1, next);
+          uint32_t r[32];
+          tc_ld_32cols(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + static_cast<uint32_t>(acc * 256 + 32 * c), r);
+          if (row_ok) finish_row32<ACT>(a, row, c0, r, raw, sa, scale + 32 * c, bias + 32 * c);
+        }
       }
       if (dead) *abort_flag = 1u;
       tc_fence_before();

@@ -1,4 +1,4 @@
-// dq_w8a8_linear for up to a few hundred tokens, on the tcgen05 tensor cores
+// dq_w8a8_linear for 9 to 128 tokens, on the tcgen05 tensor cores
 // with the operands' roles exchanged: 128 weight rows along the accumulator's
 // lanes, TOK tokens along its columns. The weights are read once whatever the
 // number of tokens up to TOK, and the tensor cores take them from shared memory
@@ -18,7 +18,6 @@
 #include "dq_launch.cuh"
 #include "tcgen05_i8.cuh"
 #include "w8a8_epilogue.cuh"
-#include "w8a8_linear_few.cuh"
 
 namespace dq {
 
@@ -170,16 +169,8 @@ __global__ void __launch_bounds__(kSplitThreads) w8a8_linear_split_kernel(const 
   // each CTA of the cluster finishes every split-th token, four rows at a time
   const int mine = (tokens - part + split - 1) / split;
   bool broken = false;
-  for (int r = 0; r < split; ++r) {
-    uint32_t at = smem_addr(const_cast<uint32_t*>(failed)), v;
-    if (split > 1) {
-      asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(at) : "r"(r));
-      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    } else {
-      v = *failed;
-    }
-    broken |= v != 0u;
-  }
+  if (split == 1) broken = *failed != 0u;
+  for (int r = 0; split > 1 && r < split; ++r) broken |= load_word(smem_addr(const_cast<uint32_t*>(failed)), r) != 0u;
   // kBatch tokens at a time: their residuals and parts are all asked for before
   // the first is used
   constexpr int kBatch = 8, kWarps = 4;
