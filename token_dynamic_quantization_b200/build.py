@@ -95,12 +95,13 @@ def build(force: bool = False, ptxas_verbose: bool = False, quiet: bool = True, 
 
 
 # Test build: the same sources with a 2 ms wait limit and one row copy (global
-# row 777 of the quantizers) and one W8A8 operand stage (tile row 1, k-tile 2)
-# left out, so that the tests can run the kernels' timeout paths. Only the
-# tests load it; the product library has none of these flags.
+# row 777 of the quantizers), one W8A8 operand stage (tile row 1, k-tile 2), one
+# tile of the paged attention's sequence 1 and one K slice of each of the linear
+# layer's kernels left out, so that the tests can run the kernels' timeout
+# paths. Only the tests load it; the product library has none of these flags.
 WAIT_TEST_LIB = os.path.join(PKG, "libdq_waittest.so")
 WAIT_TEST_DEFINES = ("DQ_WAIT_LIMIT_NS=2000000ull", "DQ_TEST_SKIP_COPY_ROW=777", "DQ_TEST_SKIP_W8A8_TILE_M=1",
-                     "DQ_TEST_SKIP_W8A8_KTILE=2")
+                     "DQ_TEST_SKIP_W8A8_KTILE=2", "DQ_TEST_SKIP_ATTENTION_SEQ=1", "DQ_TEST_SKIP_LINEAR_CHUNK=1")
 
 
 def build_wait_test(force: bool = False) -> str:

@@ -420,8 +420,17 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     };
 
     bool broken = false;  // a page outside the cache, or a copy that never came: the rows become NaN
+    bool dead = false;    // a copy never came: the warp copies nothing any more, its items become NaN
     const auto issue = [&](int st, uint32_t row) {
       broken |= row == kRowBad;
+#ifdef DQ_TEST_SKIP_ATTENTION_SEQ
+      // test builds only: leave one tile of one sequence's first key head out, so
+      // that the bounded wait for it runs out
+      if (seq == DQ_TEST_SKIP_ATTENTION_SEQ && kvh == 0 && st == 1 && warp == 0) {
+        if constexpr (kCodes) copies_commit();
+        return;
+      }
+#endif
       const uint32_t bar = smem_addr(bars + st), dst = ring + st * Shape::kStageBytes;
       if (lane == 0) mbar_arrive_expect_tx(bars + st, Shape::kStageBytes);
       if constexpr (RUN) {
@@ -470,10 +479,18 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     uint32_t in_page_next = 0u;
     int32_t page_next = -2;
     int st = 0;
+    bool opened = false;  // copies of the item's tiles have been issued
     uint2 qw[HT][KS];
+#pragma unroll
+    for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+      for (int s = 0; s < KS; ++s) qw[ht][s] = make_uint2(0u, 0u);
+    }
     const auto open = [&]() {
       enter();
       broken = false;
+      opened = !dead;
+      if (dead) return;
       const int first = t0 + warp;
       int32_t page[kStages];
       uint32_t in_page[kStages];
@@ -600,10 +617,10 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     st = 0;
     for (; tl < t1; tl += kPagedWarps) {
       const uint32_t stage = ring + st * Shape::kStageBytes;
-      if (!mbar_wait_parity(bars + st, (filled >> st) & 1u)) broken = true;
+      dead = __any_sync(0xffffffffu, dead || !mbar_wait_parity(bars + st, (filled >> st) & 1u));
       if constexpr (kCodes) copies_wait<kStages - 1>();
       __syncwarp();
-      if (__any_sync(0xffffffffu, broken)) break;
+      if (__any_sync(0xffffffffu, broken || dead)) break;
       filled ^= 1u << st;
       // ---- S^T = K Q^T
       float s[HT][MT][4];
@@ -868,12 +885,12 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       st = st + 1 == kStages ? 0 : st + 1;
     }
     if constexpr (kCodes) copies_wait<0>();
-    if (__any_sync(0xffffffffu, broken)) {
+    if (__any_sync(0xffffffffu, broken || (dead && t0 + warp < t1))) {
       // copies still on their way are waited for (each wait bounded) before the
-      // shared memory is used for anything else
-      for (int i = 0; i < kStages && tl + i * kPagedWarps < t1; ++i) {
+      // ring is used again, which it is not once a copy has failed to come
+      for (int i = 0; i < kStages && tl + i * kPagedWarps < t1 && opened; ++i) {
         const int at = st + i < kStages ? st + i : st + i - kStages;
-        mbar_wait_parity(bars + at, (filled >> at) & 1u);
+        if (!__all_sync(0xffffffffu, mbar_wait_parity(bars + at, (filled >> at) & 1u))) dead = true;
         filled ^= 1u << at;
       }
       __syncwarp();

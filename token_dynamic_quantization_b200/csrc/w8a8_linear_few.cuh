@@ -79,9 +79,16 @@ __global__ void __launch_bounds__(kFewThreads) w8a8_linear_few_kernel(const Line
     const int64_t left = a.k - (static_cast<int64_t>(chunk) * kFewChunk + warp * kFewRun);
     return chunk >= chunks || left <= 0 ? 0 : (left < kFewRun ? static_cast<int>(left) : kFewRun);
   };
+  int issued = 0;     // chunks whose copies have been issued
+  bool alive = true;  // no copy has failed to come
   const auto issue = [&](int chunk, int st) {
     const int bytes = run_bytes(chunk);
-    if (bytes == 0) return;
+    if (bytes == 0 || !alive) return;
+    issued = chunk + 1;
+#ifdef DQ_TEST_SKIP_LINEAR_CHUNK
+    // test builds only: leave one warp's run out, so that the bounded wait runs out
+    if (blockIdx.x == 1 && warp == 2 && chunk == DQ_TEST_SKIP_LINEAR_CHUNK) return;
+#endif
     if (lane == 0) mbar_arrive_expect_tx(bar + st, kFewRows * bytes);
     __syncwarp();
     if (lane < kFewRows)
@@ -121,7 +128,10 @@ __global__ void __launch_bounds__(kFewThreads) w8a8_linear_few_kernel(const Line
     __syncthreads();
     const int bytes = run_bytes(chunk);
     if (bytes > 0) {
-      if (!mbar_wait_parity(bar + st, (filled >> st) & 1u)) *failed = 1u;
+      if (chunk >= issued || !__all_sync(0xffffffffu, mbar_wait_parity(bar + st, (filled >> st) & 1u))) {
+        *failed = 1u;
+        alive = false;
+      }
       filled ^= 1u << st;
       const uint32_t wx = ring + st * kFewStage + g * kFewRowPitch + 16 * t;
       const uint32_t tx = tokens0 + buffer * kFewTokenStage + g * kFewTokenPitch + warp * kFewRun + 16 * t;

@@ -305,6 +305,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             ok = false;
             break;
           }
+#ifdef DQ_TEST_SKIP_LINEAR_CHUNK
+          // test builds only: leave one slice out, so that the MMA lane's bounded wait runs out
+          if (m0 == 256 && n0 == 0 && kt == DQ_TEST_SKIP_LINEAR_CHUNK) continue;
+#endif
           if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * (kPairA + rows_b * 128));
           const uint32_t bar = cluster_addr(full + s, 0);
           uint8_t* at = smem + s * kPairStage;
