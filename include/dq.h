@@ -335,9 +335,11 @@ typedef enum dq_activation {
  *               (the residual stream updated in place); it must not overlap
  *               `out` in any other way.
  *   out         device [m, n] of out_dtype (DQ_F32, DQ_F16, DQ_BF16).
- * m == 0 or n == 0 is a no-op. Calls of few tokens read the weights with all
- * SMs, K split over the CTAs of a cluster and the exact integer parts joined
- * through its shared memory, so the result does not depend on the split.
+ * m == 0 or n == 0 is a no-op. Up to 128 tokens the work is split by weight
+ * rows and K, not by tokens; the parts are exact integers, so a token's result
+ * depends neither on the split nor on the other tokens. k a multiple of 16 with
+ * 16-byte aligned a and b runs on the tensor cores, anything else a CUDA-core
+ * kernel with the same result but for the activations' last places.
  * Errors: as dq_w8a8_gemm (DQ_ERR_BAD_ARGUMENT for an unknown activation). */
 dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m, int64_t n, int64_t k,
                          const float* a_scale, const float* b_scale, const void* bias, dq_dtype bias_dtype,
@@ -369,7 +371,7 @@ dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m, int64_t n,
  *                DQ_BF16), or NULL for 1.
  *   epsilon      finite, >= 0.
  *   positions    device int32 [tokens].
- *   inv_freq     device float [rope_dim / 2]; NULL only with rope_dim 0.
+ *   inv_freq     device float [rope_dim / 2], finite; NULL only with rope_dim 0.
  *   rope_dim     even, 0 <= rope_dim <= head_dim.
  *   interleaved  0 or 1.
  *   q_out, k_out device, strided as q and k are. q_out may be q itself with
@@ -447,14 +449,20 @@ dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, 
  * A visible token whose page_table entry lies outside [0, num_pages), or a
  * length above max_pages * page_size, makes that sequence's rows NaN (nothing
  * outside the cache is read). Rows of the cache that no visible token names are
- * not read: they may hold anything. Sums and softmax statistics are
- * binary32; for INT8 caches the weight of a token is rounded to 11 bits
- * before it meets its codes, for 16-bit caches to the cache's precision.
+ * not used: they may hold anything. Scores are exact products summed in
+ * binary32; beside INT8 codes q is first rounded to a 16-bit integer relative to
+ * the largest channel of its head (channels within 2^-7 of it for DQ_BF16, 2^-4
+ * for DQ_F16, are exact, smaller ones within 2^-15 of it). Softmax statistics and
+ * sums are binary32. A token's weight meets its value with 16 bits beside DQ_BF16
+ * caches, with 11 beside DQ_F16 and DQ_INT8 caches; weights below 2^-30 of the
+ * largest may count as zero. A scale (or, beside INT8 codes, a query) that is
+ * infinite or NaN makes the rows that see it NaN.
  * 1 <= head_dim <= DQ_MAX_HEAD_DIM; q_heads a multiple of kv_heads, both <=
  * DQ_MAX_HEADS; 0 <= batch <= 65535 * 16, and 0 is a no-op; num_pages,
  * page_size, max_pages in [1, 2^31). Head dimensions 64, 128 and 256 with
  * 16-byte aligned tensors run on the tensor cores; others run a CUDA-core
- * kernel (binary32 weights).
+ * kernel (binary32 weights). Pages of a multiple of 16 tokens are copied in
+ * boxes, others row by row, which takes about a third longer.
  * Errors: as dq_qk_norm_rope, DQ_ERR_WORKSPACE_TOO_SMALL. */
 dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t q_stride, const void* k_cache,
                              const void* v_cache, dq_dtype cache_dtype, const float* k_scale, const float* v_scale,

@@ -6,9 +6,10 @@
 //   l <- l * exp(m_old - m) + sum_j exp(s_j - m)
 //   o <- o * exp(m_old - m) + sum_j exp(s_j - m) V_j
 // so the cache is read once, and parts of a sequence that were computed apart
-// join by the same rule. The visible tokens of a sequence are numbered 0, 1,
-// ... without the gap that a window leaves behind the first tokens, so no tile
-// holds masked tokens except the last.
+// join by the same rule. Head dimensions of 64, 128 and 256 run on the tensor
+// cores (paged_attention_mma.cuh); what follows here serves all others, and
+// unaligned tensors. It numbers the visible tokens 0, 1, ... without the gap that a
+// window leaves behind the first tokens.
 #include <cmath>
 
 #include "dq.h"
@@ -295,8 +296,9 @@ extern "C" dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t
   a.num_pages = num_pages;
   a.page_size = page_size;
   a.max_pages = max_pages;
-  a.window = window;
-  a.sinks = sinks;
+  // lengths stay below 2^31: larger numbers mean the same, and their sum cannot overflow
+  a.window = window < (int64_t(1) << 31) ? window : int64_t(1) << 31;
+  a.sinks = sinks < (int64_t(1) << 31) ? sinks : int64_t(1) << 31;
   a.softmax_scale = softmax_scale;
   a.out = out;
   a.lse = lse;

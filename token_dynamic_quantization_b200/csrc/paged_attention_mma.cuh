@@ -1,23 +1,32 @@
 // Paged decode attention on the tensor cores: one pass over the visible rows
-// of the cache, straight from global memory into the matrix operands'
-// registers.
+// of the cache with the softmax's running maximum and sum.
 //
 // One product serves up to 8 * HT query heads of a key head at once, the
 // tokens along the matrix rows so that few heads waste nothing:
-//   S^T[token, head] = K[token, :] . Q[head, :]       m16n8k16, K as the A operand
+//   S^T[token, head] = K[token, :] . Q[head, :]          K as the A operand
 //   O^T[dim, head]  += V^T[dim, token] . P[token, head]  V^T as the A operand
 // The order of the contracted index is free as long as both operands share
 // it, and so is the order of the rows of O^T. A lane (g = lane / 4, t = lane % 4)
-// therefore loads 16-byte pieces of the K rows g and g + 8 (pieces t of every 4)
-// and of the V rows of its tokens (pieces g of every 8), each used whole: no
-// shared memory and no barrier stand between the cache and the products.
+// therefore takes 16-byte pieces of the K rows g and g + 8 (pieces t of every 4)
+// and of the V rows of its tokens (pieces g of every 8), each used whole.
 // movmatrix turns P from the accumulator's layout into the B operand's.
 //
-// Codes become f16 by byte permutes: 0x64xx is 1024 + xx, so (code ^ 0x80) in the
-// low byte gives 1152 + code, and one f16 subtraction leaves the code, exact.
-// Query rows beside codes are scaled by a power of two per head into f16's
-// range; value scales are folded into the weights relative to the power of two
-// of the largest one so far, so weights keep 11 bits whatever the scales' size.
+// Rows come through shared memory: each warp has a ring of its own, filled by
+// TMA with 16 rows to a box where pages hold whole groups of 16 tokens, else with
+// four rows of any pages to a gather (64 x 8192, INT8, pages of 16: 109 us with
+// boxes, 146 with gathers), so that no warp waits for another inside an item and
+// tens of kilobytes per SM are on their way; loads of 64-byte pieces into
+// registers reach 3 TB/s, the copies close to 6.
+//
+// INT8 caches keep their codes as operands. S: Q as two signed 8-bit digits of
+// a 16-bit integer (m16n8k32, exact int32 sums). O: a code's bits plus 128 in the low
+// byte of an f16 are a subnormal, (code + 128) * 2^-24, exact in the products; an
+// operand of 128s beside the same weights collects what the 128s add up to, and
+// it is taken off every other tile, while it is small. Value scales are folded into the weights,
+// relative to the power of two of the largest one so far, so weights keep f16's 11
+// bits whatever the scales' size. bf16 caches take their weights as a bf16 and what
+// it cuts off (16 bits): one bf16 alone would round each weight at 2^-9, as large an
+// error as the output's own rounding.
 //
 // The running maximum moves only when a score exceeds it by 8 (in log2): weights
 // then stay below 2^(8 + kLift) and the rescaling of O is rare. kLift raises
@@ -27,7 +36,13 @@
 // to end, are cut into equal ranges, one per CTA, whatever the lengths; a CTA's
 // warps take its tiles in turn. Items inside one range are finished by their
 // CTA. Of an item that ranges cut, each CTA leaves (max, sum, O) in the
-// workspace, and a second kernel joins them.
+// workspace, and a second kernel joins them. Short items (the host's rule) get a
+// CTA each and need no second kernel.
+//
+// Bound by reading the cache: one sequence of 131072 tokens, bf16, 8 key heads takes
+// 91 us against 82 at the copy rate (5.9 TB/s); 64 ragged sequences of up to 8192,
+// INT8, 109 against 81 (opening the next item costs a CTA about 2 us each time,
+// and the start 5); one of 127 tokens takes 5, nearly all of it latency.
 #pragma once
 
 #include <cuda.h>
@@ -386,15 +401,16 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     }
   };
     // Token at place r of tile tl, and whether it is visible.
-    const auto token_of = [&](int tl, int r, bool& seen) -> int {
+    const auto token_of = [&](int tl, int r, bool& seen) -> uint32_t {
       const int group = tl * MT + (r >> 4);
       if (group < vis.first_groups) {
-        const int j = 16 * group + (r & 15);
-        seen = j < vis.first;
+        const uint32_t j = 16u * group + (r & 15);
+        seen = j < static_cast<uint32_t>(vis.first);
         return j;
       }
-      const int j = 16 * (group - vis.first_groups) + (vis.start & ~15) + (r & 15);
-      seen = j >= vis.start && j < vis.len;
+      // unsigned: the last tile may reach past token 2^31 - 1
+      const uint32_t j = 16u * (group - vis.first_groups) + (vis.start & ~15) + (r & 15);
+      seen = j >= static_cast<uint32_t>(vis.start) && j < static_cast<uint32_t>(vis.len);
       return j;
     };
     // Cache row numbers of a tile, in two steps so that the page table's latency
@@ -403,7 +419,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     // lane r. -2: nothing there, -1: no such page.
     const auto find_page = [&](int tl, uint32_t& in_page) -> int32_t {
       bool seen;
-      uint32_t j = static_cast<uint32_t>(token_of(tl, RUN ? 16 * lane : lane, seen));
+      const uint32_t j = token_of(tl, RUN ? 16 * lane : lane, seen);
       if constexpr (RUN) {
         seen = tl * MT + lane < vis.count && lane < MT;
       }
@@ -527,7 +543,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
     // per k-step. Beside codes as two signed 8-bit digits, 256 q1 + q0, of a
     // power of two times it, |.| <= 32639: channels down to 2^-7 (bf16; f16:
-    // 2^-4) of the head's largest are exact, the others within 2^-16 of it.
+    // 2^-4) of the head's largest are exact, the others within 2^-15 of it.
     uint32_t qf[HT][KS][2];
     float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
 #pragma unroll
@@ -709,9 +725,9 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         }
       }
       if constexpr (kCodes) {
-        float top = fmaxf(vw[0][0], vw[0][1]);
+        float top = fmaxf(fabsf(vw[0][0]), fabsf(vw[0][1]));
 #pragma unroll
-        for (int mt = 1; mt < MT; ++mt) top = max3(top, vw[mt][0], vw[mt][1]);
+        for (int mt = 1; mt < MT; ++mt) top = max3(top, fabsf(vw[mt][0]), fabsf(vw[mt][1]));
         move = top >= v_limit;
       }
 #pragma unroll
@@ -749,7 +765,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
         if constexpr (kCodes) {
           float top = 0.0f;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(vw[mt][0], vw[mt][1]));
+          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(fabsf(vw[mt][0]), fabsf(vw[mt][1])));
 #pragma unroll
           for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
           if (top >= v_limit) {

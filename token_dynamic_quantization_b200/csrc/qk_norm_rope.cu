@@ -76,9 +76,14 @@ __device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) {
 }
 
 constexpr int kNormRopeBlock = 128;
-#ifndef DQ_NR_CTAS
-#define DQ_NR_CTAS 5
-#endif
+// CTAs per SM of the vector kernel, which bounds its registers (102): 8192 tokens of
+// 32 and 8 heads of 128 channels take 35 us with 5, 35 with 4 and 40 with 6; INT8
+// pages 88, 94 and 106 us.
+constexpr int kNormRopeCtas = 5;
+// Few tokens: warps per SM that the rows of the tokens are spread over. 1003 tokens
+// of 12 and 4 heads take 5.5 us with 16, 6.8 with 8 and 7.8 with 32 (each warp
+// computes its token's angles anew).
+constexpr int kNormRopeWarps = 16;
 
 // Any head dimension, stride and alignment: one warp per (token, head row),
 // the row in registers (rotation pairs lane, lane + 32, ..., then the channels
@@ -282,8 +287,14 @@ __device__ __forceinline__ void load_weights(const void* p, int dtype, int c, fl
 // rope_dim), so the rotation needs no exchange. A token's angles are computed
 // once, each by one lane, and handed round. The next rows are loaded before the
 // current ones are worked on. Few tokens: `parts` warps share one token's rows.
+//
+// Bound by memory in the limit: 8192 tokens read and write 168 MB, 25.6 us at the
+// copy rate, and take 35 (4.8 TB/s); the same kernel without the angles takes 31
+// and as a bare copy 27. Loading two or three groups of rows ahead costs more
+// registers than it hides (36 and 38 us), and so does folding the weights into the
+// sines and cosines (36); warps that stay and walk over tokens take 40.
 template <typename T, int VEC, int CACHE, int LANES>
-__global__ void __launch_bounds__(kNormRopeBlock, DQ_NR_CTAS) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNormRopeBlock, kNormRopeCtas) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int H = VEC / 2;
   __shared__ __align__(16) float s_cos[kNormRopeBlock / 32][DQ_MAX_HEAD_DIM / 2];
   __shared__ __align__(16) float s_sin[kNormRopeBlock / 32][DQ_MAX_HEAD_DIM / 2];
@@ -537,7 +548,7 @@ dq_status launch_vector(dq::NormRopeArgs a, cudaStream_t stream) {
   while ((1 << a.lane_shift) * 2 * VEC < a.head_dim) ++a.lane_shift;
   // warps per token: one row each while the warps leave the device empty
   const int groups = (heads + (32 >> a.lane_shift) - 1) / (32 >> a.lane_shift);
-  const int64_t room = static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * 16;
+  const int64_t room = static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * dq::kNormRopeWarps;
   int64_t parts = room / a.tokens;
   a.parts = static_cast<int>(parts < 1 ? 1 : (parts > groups ? groups : parts));
   const int64_t warps = a.tokens * a.parts;

@@ -132,8 +132,8 @@ dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
                                       dq::kFewSmem, stream);
 }
 
-// 9 to 128 tokens: tiles of 128 weight rows by TOK tokens, K split
-// over the CTAs of a cluster.
+// 9 to 128 tokens, up to TOK: tiles of 128 weight rows, K split over the CTAs of
+// a cluster.
 template <int ACT, int TOK>
 dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
   using Shape = dq::SplitShape<TOK>;
@@ -143,14 +143,14 @@ dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
   if (!dq_host::make_map(&w, a.b, a.n, a.k, 128) || !dq_host::make_map(&x, a.a, a.m, a.k, TOK) ||
       !dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem))
     return dq_host::kNotLaunchable;
-  const int64_t blocks = (a.n + 127) / 128, token_blocks = (a.m + TOK - 1) / TOK;
+  const int64_t blocks = (a.n + 127) / 128;
   static std::atomic<int> known[dq_host::kMaxDevices][kMaxSplit + 1];
   int resident[kMaxSplit + 1];
   if (device < 0 || device >= dq_host::kMaxDevices) return dq_host::kNotLaunchable;
-  const int split = best_split(blocks * token_blocks, (a.k + 127) / 128,
+  const int split = best_split(blocks, (a.k + 127) / 128,
                                resident_clusters(fn, device, dq::kSplitThreads, Shape::kSmem, known[device], resident));
-  return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split), static_cast<unsigned>(token_blocks)),
-                        dq::kSplitThreads, Shape::kSmem, split, stream, w, x, a, split);
+  return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split)), dq::kSplitThreads, Shape::kSmem, split, stream, w,
+                        x, a, split);
 }
 
 // Many tokens: one pair of CTAs for every two SMs over the list of tiles.

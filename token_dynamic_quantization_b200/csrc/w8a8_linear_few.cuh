@@ -11,7 +11,7 @@
 // the rows g and g + 8 (piece t of every 64 bytes) as its A operand, every byte
 // where it lands. The tokens' codes are staged beside it, a chunk of K at a time.
 // The warps' int32 parts are exact in any order.
-// 1 x 4096 x 4096 takes 5.8 us (2.6 us to read the weights, about 2.2 for a launch);
+// 1 x 4096 x 4096 takes 5.7 us (2.6 us to read the weights, about 2.2 for a launch);
 // 5.8 with runs of 512 bytes, 7.8 with 1024, 7.2 with four stages of 256, 8.9 with
 // three stages of 512. Every wait is bounded; a sum that misses a copy becomes NaN.
 #pragma once
