@@ -462,7 +462,7 @@ dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, 
  * page_size, max_pages in [1, 2^31). Head dimensions 64, 128 and 256 with
  * 16-byte aligned tensors run on the tensor cores; others run a CUDA-core
  * kernel (binary32 weights). Pages of a multiple of 16 tokens are copied in
- * boxes, others row by row, which takes about a third longer.
+ * boxes, others row by row, which takes about a tenth longer.
  * Errors: as dq_qk_norm_rope, DQ_ERR_WORKSPACE_TOO_SMALL. */
 dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t q_stride, const void* k_cache,
                              const void* v_cache, dq_dtype cache_dtype, const float* k_scale, const float* v_scale,

@@ -8,9 +8,8 @@ namespace dq {
 
 // The item inside which a CTA's range of work units ends (seq < 0: it ends with one).
 struct PagedCut {
-  int64_t begin, tiles;  // the item's first unit, and its tiles
-  int64_t seq, item;
-  int64_t per;           // units per CTA
+  int64_t seq;           // -1: no item is cut here
+  int item, first, last; // the item of that sequence, and the CTAs of its first and last tile
 };
 
 struct PagedArgs {

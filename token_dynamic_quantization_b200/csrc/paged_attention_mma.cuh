@@ -13,10 +13,10 @@
 //
 // Rows come through shared memory: each warp has a ring of its own, filled by
 // TMA with 16 rows to a box where pages hold whole groups of 16 tokens, else with
-// four rows of any pages to a gather (64 x 8192, INT8, pages of 16: 109 us with
-// boxes, 146 with gathers), so that no warp waits for another inside an item and
-// tens of kilobytes per SM are on their way; loads of 64-byte pieces into
-// registers reach 3 TB/s, the copies close to 6.
+// four rows of any pages to a gather (64 x 8192, INT8: 108 us with pages of 16, 120
+// with pages of 20; 97 with pages of 64, whose boxes lie side by side), so that no
+// warp waits for another inside an item and tens of kilobytes per SM are on their
+// way; loads of 64-byte pieces into registers reach 3 TB/s, the copies close to 6.
 //
 // INT8 caches keep their codes as operands. S: Q as two signed 8-bit digits of
 // a 16-bit integer (m16n8k32, exact int32 sums). O: a code's bits plus 128 in the low
@@ -40,8 +40,8 @@
 // CTA each and need no second kernel.
 //
 // Bound by reading the cache: one sequence of 131072 tokens, bf16, 8 key heads takes
-// 91 us against 82 at the copy rate (5.9 TB/s); 64 ragged sequences of up to 8192,
-// INT8, 109 against 81 (opening the next item costs a CTA about 2 us each time,
+// 88 us against 82 at the copy rate (6.1 TB/s); 64 ragged sequences of up to 8192,
+// INT8, 108 against 81 (opening the next item costs a CTA about 2 us each time,
 // and the start 5); one of 127 tokens takes 5, nearly all of it latency.
 #pragma once
 
@@ -119,6 +119,16 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four neighbouring outputs, times r.
+template <typename T>
+__device__ __forceinline__ void store_row4(T* out, const float4& v, float r) {
+  if constexpr (__is_same(T, __nv_bfloat16)) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(v.x * r, v.y * r), pack_bf16(v.z * r, v.w * r));
+  } else {
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_f16(v.x * r, v.y * r), pack_f16(v.z * r, v.w * r));
+  }
 }
 
 __device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -306,7 +316,8 @@ __device__ __forceinline__ int64_t units_per_cta(int64_t total, int64_t ctas) {
 // ---------------------------------------------------------------- main kernel
 
 template <typename T, typename C, int D, int HT, bool RUN>
-__global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) paged_attention_mma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+__global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
+    paged_attention_mma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                                const PagedArgs a) {
   using Shape = PagedShape<C, D, HT>;
   constexpr bool kCodes = Shape::kCodes;
@@ -358,12 +369,11 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     }
     find_sequence<TT>(a, unit, seq, base);
   }
-  const int64_t range_begin = unit;
+  const int64_t range_begin = unit, range = unit_end - unit;
   // tokens of a tile in the order that spreads them over the banks: lane g's K
   // row, and the rows of a lane's V tokens
   const int order = token_order<Shape::kBox>(g), order_even = token_order<Shape::kBox>(2 * t);
   const int order_odd = token_order<Shape::kBox>(2 * t + 1);
-
 
   // ---- the item at hand: its tokens, heads and rows of the page table; this CTA
   // has its tiles [t0, t1)
@@ -400,138 +410,146 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       }
     }
   };
-    // Token at place r of tile tl, and whether it is visible.
-    const auto token_of = [&](int tl, int r, bool& seen) -> uint32_t {
-      const int group = tl * MT + (r >> 4);
-      if (group < vis.first_groups) {
-        const uint32_t j = 16u * group + (r & 15);
-        seen = j < static_cast<uint32_t>(vis.first);
-        return j;
-      }
-      // unsigned: the last tile may reach past token 2^31 - 1
-      const uint32_t j = 16u * (group - vis.first_groups) + (vis.start & ~15) + (r & 15);
-      seen = j >= static_cast<uint32_t>(vis.start) && j < static_cast<uint32_t>(vis.len);
+  // Token at place r of tile tl, and whether it is visible.
+  const auto token_of = [&](int tl, int r, bool& seen) -> uint32_t {
+    const int group = tl * MT + (r >> 4);
+    if (group < vis.first_groups) {
+      const uint32_t j = 16u * group + (r & 15);
+      seen = j < static_cast<uint32_t>(vis.first);
       return j;
-    };
-    // Cache row numbers of a tile, in two steps so that the page table's latency
-    // is off the path (the page, one tile ahead of the row): of its groups' first
-    // tokens in lanes 0 .. MT - 1 where pages hold whole groups, else of token r in
-    // lane r. -2: nothing there, -1: no such page.
-    const auto find_page = [&](int tl, uint32_t& in_page) -> int32_t {
-      bool seen;
-      const uint32_t j = token_of(tl, RUN ? 16 * lane : lane, seen);
-      if constexpr (RUN) {
-        seen = tl * MT + lane < vis.count && lane < MT;
-      }
-      if (tl >= t1 || !seen || lane >= TT) return -2;
-      const uint32_t p = (__umulhi(j, a.page_mul) + j) >> a.page_shift;
-      in_page = j - p * static_cast<uint32_t>(a.page_size);
-      return p < a.max_pages ? max(__ldg(table + p), -1) : -1;
-    };
-    const auto row_of = [&](int32_t page, uint32_t in_page) -> uint32_t {
-      if (page == -2) return kRowHidden;
-      if (page < 0 || page >= a.num_pages) return kRowBad;
-      return (static_cast<uint32_t>(page) * static_cast<uint32_t>(a.kv_heads) + static_cast<uint32_t>(kvh)) *
-                 static_cast<uint32_t>(a.page_size) + in_page;
-    };
+    }
+    // unsigned: the last tile may reach past token 2^31 - 1
+    const uint32_t j = 16u * (group - vis.first_groups) + (vis.start & ~15) + (r & 15);
+    seen = j >= static_cast<uint32_t>(vis.start) && j < static_cast<uint32_t>(vis.len);
+    return j;
+  };
+  // Cache row numbers of a tile, in two steps so that the page table's latency
+  // is off the path (the page, one tile ahead of the row): of its groups' first
+  // tokens in lanes 0 .. MT - 1 where pages hold whole groups, else of token r in
+  // lane r. -2: nothing there, -1: no such page.
+  const auto find_page = [&](int tl, uint32_t& in_page) -> int32_t {
+    bool seen;
+    const uint32_t j = token_of(tl, RUN ? 16 * lane : lane, seen);
+    if constexpr (RUN) {
+      seen = tl * MT + lane < vis.count && lane < MT;
+    }
+    if (tl >= t1 || !seen || lane >= TT) return -2;
+    const uint32_t p = (__umulhi(j, a.page_mul) + j) >> a.page_shift;
+    in_page = j - p * static_cast<uint32_t>(a.page_size);
+    return p < a.max_pages ? max(__ldg(table + p), -1) : -1;
+  };
+  const auto row_of = [&](int32_t page, uint32_t in_page) -> uint32_t {
+    if (page == -2) return kRowHidden;
+    if (page < 0 || page >= a.num_pages) return kRowBad;
+    return (static_cast<uint32_t>(page) * static_cast<uint32_t>(a.kv_heads) + static_cast<uint32_t>(kvh)) *
+               static_cast<uint32_t>(a.page_size) + in_page;
+  };
 
-    bool broken = false;  // a page outside the cache, or a copy that never came: the rows become NaN
-    bool dead = false;    // a copy never came: the warp copies nothing any more, its items become NaN
-    const auto issue = [&](int st, uint32_t row) {
-      broken |= row == kRowBad;
+  bool broken = false;  // a page outside the cache, or a copy that never came: the rows become NaN
+  bool dead = false;    // a copy never came: the warp copies nothing any more, its items become NaN
+  const auto issue = [&](int st, uint32_t row) {
+    broken |= row == kRowBad;
 #ifdef DQ_TEST_SKIP_ATTENTION_SEQ
-      // test builds only: leave one tile of one sequence's first key head out, so
-      // that the bounded wait for it runs out
-      if (seq == DQ_TEST_SKIP_ATTENTION_SEQ && kvh == 0 && st == 1 && warp == 0) {
-        if constexpr (kCodes) copies_commit();
-        return;
-      }
+    // test builds only: leave one tile of one sequence's first key head out, so
+    // that the bounded wait for it runs out
+    if (seq == DQ_TEST_SKIP_ATTENTION_SEQ && kvh == 0 && st == 1 && warp == 0) {
+      if constexpr (kCodes) copies_commit();
+      return;
+    }
 #endif
-      const uint32_t bar = smem_addr(bars + st), dst = ring + st * Shape::kStageBytes;
-      if (lane == 0) mbar_arrive_expect_tx(bars + st, Shape::kStageBytes);
-      if constexpr (RUN) {
-        uint32_t r[MT];
+    const uint32_t bar = smem_addr(bars + st), dst = ring + st * Shape::kStageBytes;
+    if (lane == 0) mbar_arrive_expect_tx(bars + st, Shape::kStageBytes);
+    if constexpr (RUN) {
+      uint32_t r[MT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) r[mt] = __shfl_sync(0xffffffffu, row, mt);
-        if (lane == 0) {
+      for (int mt = 0; mt < MT; ++mt) r[mt] = __shfl_sync(0xffffffffu, row, mt);
+      if (lane == 0) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int x = 0; x < Shape::kBoxes; ++x) {
-              const uint32_t to = dst + (x * TT + 16 * mt) * Shape::kBox;
-              copy_box(to, &k_map, x * (Shape::kBox / kElem), r[mt], bar);
-              copy_box(to + Shape::kRowBytes, &v_map, x * (Shape::kBox / kElem), r[mt], bar);
-            }
-          }
-        }
-        // from here on lane r's row is token r's
-        const uint32_t mine = lane < 16 ? r[0] : r[MT - 1];
-        row = mine < kRowBad ? mine + (lane & 15) : mine;
-      } else {
-        const uint32_t r0 = __shfl_sync(0xffffffffu, row, (4 * lane) & 31), r1 = __shfl_sync(0xffffffffu, row, (4 * lane + 1) & 31);
-        const uint32_t r2 = __shfl_sync(0xffffffffu, row, (4 * lane + 2) & 31), r3 = __shfl_sync(0xffffffffu, row, (4 * lane + 3) & 31);
-        if (lane < TT / 4) {
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int x = 0; x < Shape::kBoxes; ++x) {
-            const uint32_t to = dst + (x * TT + 4 * lane) * Shape::kBox;
-            gather_rows(to, &k_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
-            gather_rows(to + Shape::kRowBytes, &v_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
+            const uint32_t to = dst + (x * TT + 16 * mt) * Shape::kBox;
+            copy_box(to, &k_map, x * (Shape::kBox / kElem), r[mt], bar);
+            copy_box(to + Shape::kRowBytes, &v_map, x * (Shape::kBox / kElem), r[mt], bar);
           }
         }
       }
-      if constexpr (kCodes) {
-        if (lane < TT) {
-          const uint32_t dst = scales + st * Shape::kScaleBytes + lane * 8;
-          const uint32_t r = row < kRowBad ? row : 0u;
-          copy_async4(dst, a.k_scale + r, row < kRowBad ? 4 : 0);
-          copy_async4(dst + 4, a.v_scale + r, row < kRowBad ? 4 : 0);
+      // from here on lane r's row is token r's
+      const uint32_t mine = lane < 16 ? r[0] : r[MT - 1];
+      row = mine < kRowBad ? mine + (lane & 15) : mine;
+    } else {
+      const uint32_t r0 = __shfl_sync(0xffffffffu, row, (4 * lane) & 31), r1 = __shfl_sync(0xffffffffu, row, (4 * lane + 1) & 31);
+      const uint32_t r2 = __shfl_sync(0xffffffffu, row, (4 * lane + 2) & 31), r3 = __shfl_sync(0xffffffffu, row, (4 * lane + 3) & 31);
+      if (lane < TT / 4) {
+#pragma unroll
+        for (int x = 0; x < Shape::kBoxes; ++x) {
+          const uint32_t to = dst + (x * TT + 4 * lane) * Shape::kBox;
+          gather_rows(to, &k_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
+          gather_rows(to + Shape::kRowBytes, &v_map, x * (Shape::kBox / kElem), r0, r1, r2, r3, bar);
         }
-        copies_commit();
       }
-    };
+    }
+    if constexpr (kCodes) {
+      if (lane < TT) {
+        const uint32_t dst = scales + st * Shape::kScaleBytes + lane * 8;
+        const uint32_t r = row < kRowBad ? row : 0u;
+        copy_async4(dst, a.k_scale + r, row < kRowBad ? 4 : 0);
+        copy_async4(dst + 4, a.v_scale + r, row < kRowBad ? 4 : 0);
+      }
+      copies_commit();
+    }
+  };
 
-    // The warp's first tiles of the item into its ring, and the item's queries as
-    // they lie in memory: asked for before the previous item is joined.
-    uint32_t in_page_next = 0u;
-    int32_t page_next = -2;
-    int st = 0;
-    bool opened = false;  // copies of the item's tiles have been issued
-    uint2 qw[HT][KS];
+  // The warp's first tiles of the item into its ring, and the item's queries as
+  // they lie in memory: asked for before the previous item is joined.
+  uint32_t in_page_next = 0u;
+  int32_t page_next = -2;
+  int st = 0;
+  bool opened = false;  // copies of the item's tiles have been issued
+  uint2 qw[HT][KS];
+#pragma unroll
+  for (int ht = 0; ht < HT; ++ht) {
+#pragma unroll
+    for (int s = 0; s < KS; ++s) qw[ht][s] = make_uint2(0u, 0u);
+  }
+  const auto open = [&]() {
+    enter();
+    broken = false;
+    opened = !dead;
+    if (dead) return;
+    const int first = t0 + warp;
+    int32_t page[kStages];
+    uint32_t in_page[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) page[i] = find_page(first + i * kPagedWarps, in_page[i]);
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
+      const bool on = 8 * ht + g < heads;
+      const T* q = static_cast<const T*>(a.q) + seq * a.q_stride + static_cast<int64_t>(head0 + 8 * ht + g) * D;
 #pragma unroll
-      for (int s = 0; s < KS; ++s) qw[ht][s] = make_uint2(0u, 0u);
+      for (int s = 0; s < KS; ++s) {
+        const int c = kCodes ? (s / 4) * 64 + 16 * t + 4 * (s % 4) : (s / 2) * 32 + 8 * t + 4 * (s % 2);
+        qw[ht][s] = on ? *reinterpret_cast<const uint2*>(q + c) : make_uint2(0u, 0u);
+      }
     }
-    const auto open = [&]() {
-      enter();
-      broken = false;
-      opened = !dead;
-      if (dead) return;
-      const int first = t0 + warp;
-      int32_t page[kStages];
-      uint32_t in_page[kStages];
 #pragma unroll
-      for (int i = 0; i < kStages; ++i) page[i] = find_page(first + i * kPagedWarps, in_page[i]);
-#pragma unroll
-      for (int ht = 0; ht < HT; ++ht) {
-        const bool on = 8 * ht + g < heads;
-        const T* q = static_cast<const T*>(a.q) + seq * a.q_stride + static_cast<int64_t>(head0 + 8 * ht + g) * D;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const int c = kCodes ? (s / 4) * 64 + 16 * t + 4 * (s % 4) : (s / 2) * 32 + 8 * t + 4 * (s % 2);
-          qw[ht][s] = on ? *reinterpret_cast<const uint2*>(q + c) : make_uint2(0u, 0u);
-        }
+    for (int i = 0; i < kStages; ++i) {
+      if (first + i * kPagedWarps < t1) {
+        issue(i, row_of(page[i], in_page[i]));
+      } else if constexpr (kCodes) {
+        copies_commit();
       }
-#pragma unroll
-      for (int i = 0; i < kStages; ++i) {
-        if (first + i * kPagedWarps < t1) {
-          issue(i, row_of(page[i], in_page[i]));
-        } else if constexpr (kCodes) {
-          copies_commit();
-        }
-      }
-      page_next = find_page(first + kStages * kPagedWarps, in_page_next);
-    };
+    }
+    page_next = find_page(first + kStages * kPagedWarps, in_page_next);
+  };
+
+  // The item at hand goes on in the next CTA: its first and last tile's CTAs, for
+  // the second kernel. Every range that ends before the last one is `range` long.
+  const auto record_cut = [&]() {
+    if (t1 >= n || threadIdx.x != 0) return;
+    const int64_t first = t0 == 0 ? static_cast<int64_t>(blockIdx.x) : (item_begin + kItemCost) / range;
+    a.cuts[blockIdx.x] = {seq, item, static_cast<int>(first), static_cast<int>((item_begin + kItemCost + n - 1) / range)};
+  };
 
   enter();
   if (t1 <= t0) {  // the range is nothing but empty units: they end with it, or its item is the next CTA's
@@ -539,6 +557,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     return;
   }
   open();
+  record_cut();
   while (true) {
     // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
     // per k-step. Beside codes as two signed 8-bit digits, 256 q1 + q0, of a
@@ -944,11 +963,13 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
     const int done_head0 = head0, done_heads = heads;
     const int64_t done_seq = seq, done_begin = item_begin;
     const bool cut = t1 < n;  // the range ends inside the item
-    if (cut && threadIdx.x == 0) a.cuts[blockIdx.x] = {done_begin, n, seq, item, static_cast<int64_t>(unit_end - range_begin)};
     advance();
     const bool more = unit + kItemCost < unit_end;  // a tile of it is this CTA's
     if (!cut && !more && !a.whole && threadIdx.x == 0) a.cuts[blockIdx.x].seq = -1;
-    if (more) open();
+    if (more) {
+      open();
+      record_cut();
+    }
     __syncthreads();  // every warp has left its part
     float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (done_begin + kItemCost < range_begin ? 0 : 1)) *
                                 static_cast<int64_t>(Shape::kPartFloats);
@@ -972,14 +993,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
       if (complete) {
         const int64_t at = done_seq * a.q_heads + done_head0 + h;
         const float r = empty ? 0.0f : 1.0f / total;
-        T* out = static_cast<T*>(a.out) + at * D + c;
-        uint2 w;
-        if constexpr (__is_same(T, __nv_bfloat16)) {
-          w = make_uint2(pack_bf16(sum.x * r, sum.y * r), pack_bf16(sum.z * r, sum.w * r));
-        } else {
-          w = make_uint2(pack_f16(sum.x * r, sum.y * r), pack_f16(sum.z * r, sum.w * r));
-        }
-        *reinterpret_cast<uint2*>(out) = w;
+        store_row4(static_cast<T*>(a.out) + at * D + c, sum, r);
         if (a.lse != nullptr && c == 0)
           a.lse[at] = empty ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
       } else {
@@ -999,62 +1013,96 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas)) 
 
 constexpr int kPagedJoinThreads = 512;
 
-// Joins what CTAs have left of the items that their ranges cut: one CTA per
-// border between two ranges; the first border inside an item takes it. A head
-// takes D / 4 threads, and what threads are left share its parts.
+// Joins what CTAs have left of the items that their ranges cut. There is one CTA
+// per border between two ranges, and those inside an item share its heads. A head
+// takes D / 4 threads, each up to kBatch parts whose loads are all on their way
+// at once; of an item with more parts, several such rows, joined through shared memory.
+// It adds 3 us to the main kernel, most of them two trips to L2 (1 x 131072 bf16: 87.6 us
+// in all, 83.9 without it; 90.9 with one border doing all heads, a part after the
+// other; 89 with kBatch 2, and 88 with 8, whose registers delay the CTAs' start).
 template <typename T, typename C, int D, int HT>
 __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel(const PagedArgs a) {
   using Shape = PagedShape<C, D, HT>;
-  constexpr int kHeads = Shape::kHeads, kVec = D / 4, kRows = kPagedJoinThreads / kVec;
-  __shared__ float s_o[kRows][D];
+  constexpr int kHeads = Shape::kHeads, kVec = D / 4, kRows = kPagedJoinThreads / kVec, kBatch = 4;
+  static_assert(kRows >= kHeads, "a row per head");
+  __shared__ __align__(16) float s_o[kRows][D];
   __shared__ float s_m[kRows], s_l[kRows];
   pdl_launch_dependents();
   pdl_wait_primary();
   const PagedCut cut = a.cuts[blockIdx.x];
   if (cut.seq < 0) return;
-  const int64_t c0 = (cut.begin + kItemCost) / cut.per, c1 = (cut.begin + kItemCost + cut.tiles - 1) / cut.per;
-  if (c0 != static_cast<int64_t>(blockIdx.x)) return;
-  const int kvh = static_cast<int>(cut.item) / a.head_sets, set = static_cast<int>(cut.item) - kvh * a.head_sets;
+  const int kvh = cut.item / a.head_sets, set = cut.item - kvh * a.head_sets;
   const int heads = a.group - set * kHeads < kHeads ? a.group - set * kHeads : kHeads;
-  const int vec = threadIdx.x % kVec, row = threadIdx.x / kVec;
-  const int splits = kRows / heads, h = row % heads, split = row / heads;  // kRows >= kHeads
+  const int parts = cut.last - cut.first + 1;
+  // this border has heads share, share + sharers, ...
+  const int share = static_cast<int>(blockIdx.x) - cut.first, sharers = parts - 1 < heads ? parts - 1 : heads;
+  if (share >= sharers) return;
+  const int mine = (heads - share + sharers - 1) / sharers;
+  const int want = (parts + kBatch - 1) / kBatch, splits = want * mine <= kRows ? want : kRows / mine;
+  const int vec = threadIdx.x % kVec, row = threadIdx.x / kVec, split = row / mine;
+  const int h = share + (row - split * mine) * sharers;
 
   float top = -INFINITY, sum_l = 0.0f;
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (split < splits) {
-#pragma unroll 8
-    for (int64_t c = c0 + split; c <= c1; c += splits) {
-      const float* part = a.parts + (c * 2 + (c == c0 ? 1 : 0)) * static_cast<int64_t>(Shape::kPartFloats);
-      const float2 st = *reinterpret_cast<const float2*>(part + kHeads * D + 2 * h);
-      const float4 v = *reinterpret_cast<const float4*>(part + h * D + 4 * vec);
-      const float next = fmaxf(top, st.x);
-      const float keep = top == next ? 1.0f : exp2f(top - next), f = st.x == next ? 1.0f : exp2f(st.x - next);
-      sum_l = fmaf(st.y, f, sum_l * keep);
-      sum.x = fmaf(v.x, f, sum.x * keep);
-      sum.y = fmaf(v.y, f, sum.y * keep);
-      sum.z = fmaf(v.z, f, sum.z * keep);
-      sum.w = fmaf(v.w, f, sum.w * keep);
+    for (int c0 = cut.first + split; c0 <= cut.last; c0 += kBatch * splits) {
+      float2 st[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t c = c0 + i * splits;
+        st[i] = make_float2(-INFINITY, 0.0f);
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c <= cut.last) {
+          const float* part = a.parts + (c * 2 + (c == cut.first ? 1 : 0)) * static_cast<int64_t>(Shape::kPartFloats);
+          st[i] = *reinterpret_cast<const float2*>(part + kHeads * D + 2 * h);
+          v[i] = *reinterpret_cast<const float4*>(part + h * D + 4 * vec);
+        }
+      }
+      float next = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) next = fmaxf(next, st[i].x);
+      const float keep = top == next ? 1.0f : exp2f(top - next);
+      sum_l *= keep;
+      sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float f = st[i].x == next ? 1.0f : exp2f(st[i].x - next);
+        sum_l = fmaf(st[i].y, f, sum_l);
+        sum.x = fmaf(v[i].x, f, sum.x);
+        sum.y = fmaf(v[i].y, f, sum.y);
+        sum.z = fmaf(v[i].z, f, sum.z);
+        sum.w = fmaf(v[i].w, f, sum.w);
+      }
       top = next;
     }
   }
-  *reinterpret_cast<float4*>(&s_o[row][4 * vec]) = sum;
-  if (vec == 0) {
-    s_m[row] = top;
-    s_l[row] = sum_l;
-  }
-  __syncthreads();
-  for (int x = threadIdx.x; x < heads * D; x += kPagedJoinThreads) {
-    const int hx = x / D, c = x - hx * D;
-    float all = -INFINITY, total = 0.0f, r = 0.0f;
-    for (int p = hx; p < splits * heads; p += heads) all = fmaxf(all, s_m[p]);
-    for (int p = hx; p < splits * heads; p += heads) {
-      const float f = s_m[p] == all ? 1.0f : exp2f(s_m[p] - all);
-      total = fmaf(s_l[p], f, total);
-      r = fmaf(s_o[p][c], f, r);
+  if (splits > 1) {
+    *reinterpret_cast<float4*>(&s_o[row][4 * vec]) = sum;
+    if (vec == 0) {
+      s_m[row] = top;
+      s_l[row] = sum_l;
     }
-    const int64_t at = cut.seq * a.q_heads + kvh * a.group + set * kHeads + hx;
-    static_cast<T*>(a.out)[at * D + c] = static_cast<T>(r / total);
-    if (c == 0 && a.lse != nullptr) a.lse[at] = ((all == -INFINITY ? 0.0f : all) - kLift + log2f(total)) * kLn2;
+    __syncthreads();
+    if (split == 0) {
+      for (int p = row + mine; p < splits * mine; p += mine) top = fmaxf(top, s_m[p]);
+      sum_l = 0.0f;
+      sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int p = row; p < splits * mine; p += mine) {
+        const float f = s_m[p] == top ? 1.0f : exp2f(s_m[p] - top);
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[p][4 * vec]);
+        sum_l = fmaf(s_l[p], f, sum_l);
+        sum.x = fmaf(v.x, f, sum.x);
+        sum.y = fmaf(v.y, f, sum.y);
+        sum.z = fmaf(v.z, f, sum.z);
+        sum.w = fmaf(v.w, f, sum.w);
+      }
+    }
+  }
+  if (split == 0) {
+    const int64_t at = cut.seq * a.q_heads + kvh * a.group + set * kHeads + h;
+    store_row4(static_cast<T*>(a.out) + at * D + 4 * vec, sum, 1.0f / sum_l);
+    if (vec == 0 && a.lse != nullptr) a.lse[at] = ((top == -INFINITY ? 0.0f : top) - kLift + log2f(sum_l)) * kLn2;
   }
 }
 
