@@ -452,7 +452,7 @@ dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, 
  * not used: they may hold anything. Scores are exact products summed in
  * binary32; beside INT8 codes q is first rounded to a 16-bit integer relative to
  * the largest channel of its head (channels within 2^-7 of it for DQ_BF16, 2^-4
- * for DQ_F16, are exact, smaller ones within 2^-15 of it). Softmax statistics and
+ * for DQ_F16, are exact, smaller ones within 0.5 / 16319 of it). Softmax statistics and
  * sums are binary32. A token's weight meets its value with 16 bits beside DQ_BF16
  * caches, with 11 beside DQ_F16 and DQ_INT8 caches; weights below 2^-30 of the
  * largest may count as zero. A scale (or, beside INT8 codes, a query) that is

@@ -79,3 +79,17 @@ def test_attention_tile_timeout(libs, monkeypatch, cache, lengths):
     assert not bad[0].any()
     assert torch.equal(got[~bad], want[~bad]) and not want.isnan().any()
     assert torch.equal(call(libs[0], s), want)
+
+
+@pytest.mark.parametrize("cache", [torch.int8, torch.bfloat16])
+@pytest.mark.parametrize("longest", [200, 900])
+def test_attention_tile_timeout_of_single_warps(libs, monkeypatch, cache, longest):
+    from test_paged_attention_gpu import call, make
+
+    s = make([longest - i for i in range(130)], 32, 8, 128, torch.bfloat16, cache, 16, seed=4)
+    want, got = _both(libs, monkeypatch, lambda dq: call(dq, s))
+    bad = got.isnan().all(-1)
+    assert got.isnan().any(-1).equal(bad)
+    assert bad[1, :4].all() and not bad[0].any()
+    assert torch.equal(got[~bad], want[~bad]) and not want.isnan().any()
+    assert torch.equal(call(libs[0], s), want)

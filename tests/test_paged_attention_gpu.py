@@ -3,7 +3,11 @@
 Tolerances, derived from the arithmetic. A score is a binary32 sum of head_dim
 products that are exact (16-bit or code times 16-bit), scaled by a few rounded
 factors: off by at most ds = (head_dim + 8) * 2^-23 * |scale| sum_c |q_c K_c| (a
-sum's rounding may truncate), which changes its weight by the factor exp(ds);
+sum's rounding may truncate), which changes its weight by the factor exp(ds).
+Beside codes a query is first rounded to integers, a power of two times it, of
+which the head's largest lies in [16319, 32639]: each channel is off by at most
+half a unit, 0.5 / 16319 max_c |q_c|, and ds grows by |scale| 0.5 / 16319 max_c
+|q_c| sum_c |K_c|. Next,
 the weight's own exponential, and the running rescalings and sums, are within
 2^-18 in all. A weight is rounded to u_p relative before it meets its values:
 2^-11 for f16 and INT8 caches, 2^-8 for bf16 (less where it is kept in two
@@ -87,6 +91,9 @@ def verify(s, out, lse=None, window=0, sinks=0, scale=None):
         q = s["q"][i].double()
         score = torch.einsum("hd,nhd->hn", q, k) * scale
         ds = ((dim + 8) * 2.0**-23 * abs(scale) * torch.einsum("hd,nhd->hn", q.abs(), k.abs())).amax(-1)
+        if codes:
+            step = 0.5 / 16319 * q.abs().amax(-1) * abs(scale)
+            ds = ds + step * k.abs().sum(-1).amax(0)
         p = torch.softmax(score, -1)
         want = torch.einsum("hn,nhd->hd", p, v)
         a = torch.einsum("hn,nhd->hd", p, v.abs())

@@ -129,8 +129,8 @@ dq_status launch_generic(const dq::PagedArgs& a, cudaStream_t stream) {
 // and the accumulators fit (16 heads of 256 channels do not).
 constexpr int head_tiles(int group, int dim) { return group > 8 && dim <= 128 ? 2 : 1; }
 
-// CTAs that share the tiles at most: what fits the device at once, four to an SM.
-int64_t most_ctas() { return static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * 4; }
+// CTAs that share the tiles at most: what fits the device at once, eight to an SM.
+int64_t most_ctas() { return static_cast<int64_t>(dq_host::sm_count(dq_host::current_device())) * 8; }
 
 bool mma_dim(int dim) { return dim == 64 || dim == 128 || dim == 256; }
 
@@ -173,10 +173,10 @@ dq_status launch_pdl(Kernel kernel, dim3 grid, int block, size_t smem, cudaStrea
   return dq_host::launch_status();
 }
 
-template <typename T, typename C, int D, int HT, bool RUN>
+template <typename T, typename C, int D, int HT, bool RUN, int W>
 dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
-  using Shape = dq::PagedShape<C, D, HT>;
-  auto fn = dq::paged_attention_mma_kernel<T, C, D, HT, RUN>;
+  using Shape = dq::PagedShape<C, D, HT, W>;
+  auto fn = dq::paged_attention_mma_kernel<T, C, D, HT, RUN, W>;
   CUtensorMap k_map, v_map;
   const int64_t rows = a.num_pages * a.kv_heads * a.page_size;
   if (!rows_map<C, Shape::kBox>(&k_map, a.k_cache, rows, D, RUN ? 16 : 1) ||
@@ -184,29 +184,47 @@ dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
     return dq_host::kNotLaunchable;
   const int device = dq_host::current_device();
   if (!dq_host::allow_smem_bytes(reinterpret_cast<const void*>(fn), device, Shape::kSmem)) return dq_host::kNotLaunchable;
-  a.head_sets = (a.group + Shape::kHeads - 1) / Shape::kHeads;
   int64_t ctas = static_cast<int64_t>(dq_host::sm_count(device)) *
-                 dq_host::blocks_per_sm(reinterpret_cast<const void*>(fn), dq::kPagedThreads, Shape::kSmem, device);
+                 dq_host::blocks_per_sm(reinterpret_cast<const void*>(fn), Shape::kThreads, Shape::kSmem, device);
   if (ctas > most_ctas()) ctas = most_ctas();
-  // short sequences: a CTA per item, nothing to join. With at most four tiles for
-  // each warp there is little to share, and one launch less (1 sequence of 127 tokens,
-  // 8 key heads, INT8: 5.0 us against 7.0).
-  const int64_t room = a.max_pages * a.page_size;
-  const int64_t most_seen = a.window != 0 && a.window + a.sinks < room ? a.window + a.sinks + 32 : room;
-  const int64_t items = a.batch * a.kv_heads * a.head_sets;
-  a.whole = most_seen <= int64_t(4) * dq::kPagedWarps * Shape::kTokens && items < (int64_t(1) << 31) ? 1 : 0;
-  if (a.whole)
-    return launch_pdl(fn, dim3(static_cast<unsigned>(items)), dq::kPagedThreads, Shape::kSmem, stream, k_map, v_map, a);
+  if (a.whole) {
+    const dim3 items(static_cast<unsigned>(a.batch * a.kv_heads * a.head_sets));
+    return launch_pdl(fn, items, Shape::kThreads, Shape::kSmem, stream, k_map, v_map, a);
+  }
   a.cuts = reinterpret_cast<dq::PagedCut*>(a.parts + most_ctas() * 2 * Shape::kPartFloats);
-  const dq_status st = launch_pdl(fn, dim3(static_cast<unsigned>(ctas)), dq::kPagedThreads, Shape::kSmem, stream, k_map, v_map, a);
+  const dim3 grid(static_cast<unsigned>(ctas));
+  const dq_status st = launch_pdl(fn, grid, Shape::kThreads, Shape::kSmem, stream, k_map, v_map, a);
   if (st != DQ_OK) return st;
   return launch_pdl(dq::paged_attention_join_kernel<T, C, D, HT>, dim3(static_cast<unsigned>(ctas - 1)),
                     dq::kPagedJoinThreads, 0, stream, a);
 }
 
+// How the work is cut, from the number of items (sequence, key head, head set)
+// and the most tiles that one can have.
+//   up to 16 tiles: an item is a CTA's, whole, and there is nothing to join (1
+// sequence of 127 tokens, INT8: 5.0 us against 7.0 in ranges; 444 x 100: 28 against 39);
+// longer ones are cut into ranges.
+//   six items per SM or more, whole: a CTA is one warp, else four that share the
+// item. 444 sequences of up to 100 tokens, 8 key heads, take 27 us (bf16) and 28 (INT8)
+// with one warp, 54 and 60 with four; 32 to 128 sequences have too few items.
+//   six items per SM or more, cut into ranges: one warp for INT8 caches of 128 or
+// 256 channels (444 x 600 tokens 79 us against 101, 128 x 600 33 against 36, 256 x 1000 of 256
+// channels 119 against 133, but with fewer items 64 x 4160 66 against 65 and 32 x 600
+// 18 against 15), four for 16-bit caches (256 x 1000: 94 us, one warp 101) and 64
+// channels (256 x 1000 INT8: 56 us, one warp 64).
 template <typename T, typename C, int D, int HT>
-dq_status by_pages(const dq::PagedArgs& a, cudaStream_t stream) {
-  return a.page_size % 16 == 0 ? launch_mma<T, C, D, HT, true>(a, stream) : launch_mma<T, C, D, HT, false>(a, stream);
+dq_status by_pages(dq::PagedArgs a, cudaStream_t stream) {
+  using Shape = dq::PagedShape<C, D, HT, 4>;
+  a.head_sets = (a.group + Shape::kHeads - 1) / Shape::kHeads;
+  const int64_t room = a.max_pages * a.page_size;
+  const int64_t most_seen = a.window != 0 && a.window + a.sinks < room ? a.window + a.sinks + 32 : room;
+  a.whole = most_seen <= 16 * Shape::kTokens ? 1 : 0;
+  const int64_t items = a.batch * a.kv_heads * a.head_sets;
+  const bool many = items >= int64_t(6) * dq_host::sm_count(dq_host::current_device());
+  const bool run = a.page_size % 16 == 0;
+  if (many && (a.whole || (Shape::kCodes && D >= 128)))
+    return run ? launch_mma<T, C, D, HT, true, 1>(a, stream) : launch_mma<T, C, D, HT, false, 1>(a, stream);
+  return run ? launch_mma<T, C, D, HT, true, 4>(a, stream) : launch_mma<T, C, D, HT, false, 4>(a, stream);
 }
 
 template <typename T, typename C>

@@ -37,12 +37,13 @@
 // warps take its tiles in turn. Items inside one range are finished by their
 // CTA. Of an item that ranges cut, each CTA leaves (max, sum, O) in the
 // workspace, and a second kernel joins them. Short items (the host's rule) get a
-// CTA each and need no second kernel.
+// CTA each and need no second kernel. Where there are many items (the host's
+// rule), a CTA is a single warp: no warp waits for another when an item ends.
 //
 // Bound by reading the cache: one sequence of 131072 tokens, bf16, 8 key heads takes
 // 88 us against 82 at the copy rate (6.1 TB/s); 64 ragged sequences of up to 8192,
 // INT8, 108 against 81 (opening the next item costs a CTA about 2 us each time,
-// and the start 5); one of 127 tokens takes 5, nearly all of it latency.
+// and the start 5); 200 of up to 8000, INT8, 297 against 259; one of 127 tokens takes 5, nearly all of it latency.
 #pragma once
 
 #include <cuda.h>
@@ -55,14 +56,14 @@
 
 namespace dq {
 
-constexpr int kPagedWarps = 4;
-constexpr int kPagedThreads = kPagedWarps * 32;
 constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the running maximum
 constexpr float kLift = 6.0f;   // log2 of the weight at the running maximum
 constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;  // row numbers outside every cache
 
-template <typename C, int D, int HT>
+// W: warps of a CTA, which share an item's tiles.
+template <typename C, int D, int HT, int W>
 struct PagedShape {
+  static constexpr int kThreads = 32 * W;
   static constexpr bool kCodes = sizeof(C) == 1;
   static constexpr int kTokens = kCodes && D <= 128 ? 32 : 16;
   static constexpr int kHeads = 8 * HT;
@@ -70,7 +71,7 @@ struct PagedShape {
   static constexpr int kPartFloats = kHeads * D + 2 * kHeads;
   // CTAs per SM: three, and two where their rings would be too short (codes of 128
   // channels: 109 us with two, 115 with three) or the registers do not allow more
-  static constexpr int kCtas = HT * D > 128 || (kCodes && D == 128) ? 2 : 3;
+  static constexpr int kCtas = (HT * D > 128 || (kCodes && D == 128) ? 2 : 3) * 4 / W;
   // rows lie in shared memory in boxes of 128 bytes (64 for 64 codes), swizzled
   static constexpr int kBox = D * int(sizeof(C)) < 128 ? D * int(sizeof(C)) : 128;
   static constexpr int kBoxes = D * int(sizeof(C)) / kBox;
@@ -79,12 +80,12 @@ struct PagedShape {
   static constexpr int kScaleBytes = kCodes ? 2 * 4 * kTokens : 0;
   static constexpr int kStageBytes = 2 * kRowBytes;
   static constexpr int kPitch = D + 4;                      // of a head's row there, against bank conflicts
-  static constexpr int kJoin = kPagedWarps * (kHeads * kPitch + 2 * kHeads) * 4;
-  static constexpr int kFit = (227 * 1024 / kCtas - 2048 - 256 - kJoin) / kPagedWarps / (kStageBytes + kScaleBytes);
+  static constexpr int kJoin = W * (kHeads * kPitch + 2 * kHeads) * 4;
+  static constexpr int kFit = (227 * 1024 / kCtas - 2048 - 256 - kJoin) / W / (kStageBytes + kScaleBytes);
   static constexpr int kStages = kFit < 2 ? 2 : (kFit > 8 ? 8 : kFit);
-  static constexpr int kRings = kPagedWarps * kStages * kStageBytes;
-  static constexpr int kScales = kPagedWarps * kStages * kScaleBytes;
-  static constexpr int kBarriers = kPagedWarps * kStages * 8;
+  static constexpr int kRings = W * kStages * kStageBytes;
+  static constexpr int kScales = W * kStages * kScaleBytes;
+  static constexpr int kBarriers = W * kStages * 8;
   static constexpr int kBody = kRings + kScales + kJoin;
   static constexpr size_t kSmem = 1024 + size_t(kBody) + kBarriers;  // 1024: alignment of the swizzle pattern
 };
@@ -248,10 +249,13 @@ __device__ __forceinline__ Groups visible_groups(const PagedArgs& a, int len) {
 }
 
 // Opening and joining an item takes a CTA as long as several tiles (3.4 us against
-// 0.6 us a tile on 64 sequences of up to 8192 tokens): ranges are cut in units of
-// which an item has kItemCost more than tiles, the first ones empty. On those
-// sequences, INT8, 137 us with 0, 119 with 4, 115 with 6 and 10.
-constexpr int kItemCost = 8;
+// 0.6 us a tile on 64 sequences of up to 8192 tokens, four warps): ranges are cut
+// in units of which an item has kItemCost more than tiles, the first ones empty. On
+// those sequences, INT8, 137 us with 0, 119 with 4, 115 with 6 and 10. A warp by itself
+// takes longer for a tile: 444 sequences of up to 600 tokens take 87 us with 1, 79
+// with 2, 81 with 4.
+template <int W>
+constexpr int kItemCost = W == 4 ? 8 : 2;
 
 // Tiles of one sequence's item; a sequence without tokens still has one, whose
 // CTA writes its zeros.
@@ -260,9 +264,9 @@ __device__ __forceinline__ int tiles_of(const Groups& v) {
   constexpr int kGroups = TT / 16;
   return v.count == 0 ? 1 : (v.count + kGroups - 1) / kGroups;
 }
-template <int TT>
+template <int TT, int W>
 __device__ __forceinline__ int64_t item_units(const PagedArgs& a, int64_t b) {
-  return tiles_of<TT>(visible_groups(a, a.lengths[b])) + kItemCost;
+  return tiles_of<TT>(visible_groups(a, a.lengths[b])) + kItemCost<W>;
 }
 
 __device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
@@ -272,23 +276,23 @@ __device__ __forceinline__ int64_t warp_sum_i64(int64_t v) {
 }
 
 // All units of the call (every lane of the warp gets the sum).
-template <int TT>
+template <int TT, int W>
 __device__ int64_t total_units(const PagedArgs& a) {
   int64_t sum = 0;
   const int lane = threadIdx.x & 31;
-  for (int64_t b = lane; b < a.batch; b += 32) sum += item_units<TT>(a, b);
+  for (int64_t b = lane; b < a.batch; b += 32) sum += item_units<TT, W>(a, b);
   return warp_sum_i64(sum) * a.kv_heads * a.head_sets;
 }
 
 // The sequence that unit `x` belongs to, and the number of its first unit.
-template <int TT>
+template <int TT, int W>
 __device__ void find_sequence(const PagedArgs& a, int64_t x, int64_t& seq, int64_t& base) {
   const int lane = threadIdx.x & 31;
   const int64_t per = static_cast<int64_t>(a.kv_heads) * a.head_sets;
   int64_t before = 0;
   for (int64_t b0 = 0;; b0 += 32) {
     const int64_t b = b0 + lane;
-    int64_t end = b < a.batch ? item_units<TT>(a, b) * per : 0;
+    int64_t end = b < a.batch ? item_units<TT, W>(a, b) * per : 0;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int64_t up = __shfl_up_sync(0xffffffffu, end, o);
@@ -308,18 +312,20 @@ __device__ void find_sequence(const PagedArgs& a, int64_t x, int64_t& seq, int64
 }
 
 // Units per CTA: equal shares, and at least a short item for each.
+template <int W>
 __device__ __forceinline__ int64_t units_per_cta(int64_t total, int64_t ctas) {
   const int64_t per = (total + ctas - 1) / ctas;
-  return per < kItemCost + kPagedWarps ? kItemCost + kPagedWarps : per;
+  return per < kItemCost<W> + W ? kItemCost<W> + W : per;
 }
 
 // ---------------------------------------------------------------- main kernel
 
-template <typename T, typename C, int D, int HT, bool RUN>
-__global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
+template <typename T, typename C, int D, int HT, bool RUN, int W>
+__global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
     paged_attention_mma_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                                const PagedArgs a) {
-  using Shape = PagedShape<C, D, HT>;
+  using Shape = PagedShape<C, D, HT, W>;
+  constexpr int kItemCost = dq::kItemCost<W>;
   constexpr bool kCodes = Shape::kCodes;
   constexpr bool kBf16 = !kCodes && sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
   constexpr int TT = Shape::kTokens, MT = TT / 16, kHeads = Shape::kHeads;
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // the warps' rings and scales; what they leave of an item, [warps][kHeads][D] and [warps][kHeads][2]
   float* s_o = reinterpret_cast<float*>(smem + Shape::kRings + Shape::kScales);
-  float* s_stat = s_o + kPagedWarps * kHeads * Shape::kPitch;
+  float* s_stat = s_o + W * kHeads * Shape::kPitch;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t ring = smem_addr(smem) + warp * kStages * Shape::kStageBytes;
@@ -354,20 +360,20 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
   const int items_per_seq = a.kv_heads * a.head_sets;
   if (a.whole) {
     seq = blockIdx.x / items_per_seq;
-    const int64_t n = item_units<TT>(a, seq);
+    const int64_t n = item_units<TT, W>(a, seq);
     base = 0;
     unit = (blockIdx.x - seq * items_per_seq) * n;
     unit_end = unit + n;
   } else {
-    const int64_t total = total_units<TT>(a);
-    const int64_t per = units_per_cta(total, gridDim.x);
+    const int64_t total = total_units<TT, W>(a);
+    const int64_t per = units_per_cta<W>(total, gridDim.x);
     unit = per * blockIdx.x;
     unit_end = unit + per < total ? unit + per : total;
     if (unit >= total) {
       if (threadIdx.x == 0) a.cuts[blockIdx.x].seq = -1;
       return;
     }
-    find_sequence<TT>(a, unit, seq, base);
+    find_sequence<TT, W>(a, unit, seq, base);
   }
   const int64_t range_begin = unit, range = unit_end - unit;
   // tokens of a tile in the order that spreads them over the banks: lane g's K
@@ -521,7 +527,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
     int32_t page[kStages];
     uint32_t in_page[kStages];
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) page[i] = find_page(first + i * kPagedWarps, in_page[i]);
+    for (int i = 0; i < kStages; ++i) page[i] = find_page(first + i * W, in_page[i]);
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       const bool on = 8 * ht + g < heads;
@@ -534,13 +540,13 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
     }
 #pragma unroll
     for (int i = 0; i < kStages; ++i) {
-      if (first + i * kPagedWarps < t1) {
+      if (first + i * W < t1) {
         issue(i, row_of(page[i], in_page[i]));
       } else if constexpr (kCodes) {
         copies_commit();
       }
     }
-    page_next = find_page(first + kStages * kPagedWarps, in_page_next);
+    page_next = find_page(first + kStages * W, in_page_next);
   };
 
   // The item at hand goes on in the next CTA: its first and last tile's CTAs, for
@@ -562,7 +568,8 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
     // Q as the B operand, head g. Beside a 16-bit cache as it is, four channels
     // per k-step. Beside codes as two signed 8-bit digits, 256 q1 + q0, of a
     // power of two times it, |.| <= 32639: channels down to 2^-7 (bf16; f16:
-    // 2^-4) of the head's largest are exact, the others within 2^-15 of it.
+    // 2^-4) of the head's largest are exact, the others off by at most
+    // half a unit, 0.5 / 16319 of it.
     uint32_t qf[HT][KS][2];
     float q_mul[HT][2];  // scores' factor of heads 2t and 2t + 1, log2(e) included
 #pragma unroll
@@ -650,7 +657,7 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
     };
     int tl = t0 + warp;
     st = 0;
-    for (; tl < t1; tl += kPagedWarps) {
+    for (; tl < t1; tl += W) {
       const uint32_t stage = ring + st * Shape::kStageBytes;
       dead = __any_sync(0xffffffffu, dead || !mbar_wait_parity(bars + st, (filled >> st) & 1u));
       if constexpr (kCodes) copies_wait<kStages - 1>();
@@ -911,19 +918,19 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
       }
       // ---- refill the stage; its table entries were asked for one tile ago
       __syncwarp();
-      if (tl + kStages * kPagedWarps < t1) {
+      if (tl + kStages * W < t1) {
         issue(st, row_of(page_next, in_page_next));
       } else if constexpr (kCodes) {
         copies_commit();
       }
-      page_next = find_page(tl + (kStages + 1) * kPagedWarps, in_page_next);
+      page_next = find_page(tl + (kStages + 1) * W, in_page_next);
       st = st + 1 == kStages ? 0 : st + 1;
     }
     if constexpr (kCodes) copies_wait<0>();
     if (__any_sync(0xffffffffu, broken || (dead && t0 + warp < t1))) {
       // copies still on their way are waited for (each wait bounded) before the
       // ring is used again, which it is not once a copy has failed to come
-      for (int i = 0; i < kStages && tl + i * kPagedWarps < t1 && opened; ++i) {
+      for (int i = 0; i < kStages && tl + i * W < t1 && opened; ++i) {
         const int at = st + i < kStages ? st + i : st + i - kStages;
         if (!__all_sync(0xffffffffu, mbar_wait_parity(bars + at, (filled >> at) & 1u))) dead = true;
         filled ^= 1u << at;
@@ -973,14 +980,14 @@ __global__ void __launch_bounds__(kPagedThreads, (PagedShape<C, D, HT>::kCtas))
     __syncthreads();  // every warp has left its part
     float* part = a.parts + (static_cast<int64_t>(blockIdx.x) * 2 + (done_begin + kItemCost < range_begin ? 0 : 1)) *
                                 static_cast<int64_t>(Shape::kPartFloats);
-    for (int x = threadIdx.x; x < done_heads * (D / 4); x += kPagedThreads) {
+    for (int x = threadIdx.x; x < done_heads * (D / 4); x += 32 * W) {
       const int h = x / (D / 4), c = (x - h * (D / 4)) * 4;
       float top = -INFINITY, total = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) top = fmaxf(top, s_stat[(w * kHeads + h) * 2]);
+      for (int w = 0; w < W; ++w) top = fmaxf(top, s_stat[(w * kHeads + h) * 2]);
       float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kPagedWarps; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float mw = s_stat[(w * kHeads + h) * 2];
         const float f = mw == top ? 1.0f : exp2f(mw - top);
         total = fmaf(s_stat[(w * kHeads + h) * 2 + 1], f, total);
@@ -1022,7 +1029,7 @@ constexpr int kPagedJoinThreads = 512;
 // other; 89 with kBatch 2, and 88 with 8, whose registers delay the CTAs' start).
 template <typename T, typename C, int D, int HT>
 __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel(const PagedArgs a) {
-  using Shape = PagedShape<C, D, HT>;
+  using Shape = PagedShape<C, D, HT, 4>;
   constexpr int kHeads = Shape::kHeads, kVec = D / 4, kRows = kPagedJoinThreads / kVec, kBatch = 4;
   static_assert(kRows >= kHeads, "a row per head");
   __shared__ __align__(16) float s_o[kRows][D];
