@@ -467,6 +467,9 @@ def _rows(name: str, t, shape, dtype, index: int):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    row, head, one = t.stride()
+    if one == 1 and head == shape[2] and row >= shape[1] * head:
+        return t.data_ptr(), row
     return t.data_ptr(), _row_stride(name, t)
 
 
@@ -560,15 +563,16 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, epsilo
             return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, epsilon, interleaved, out, None, check)
     if out is None:
         q_out, k_out = q.new_empty(q_shape), q.new_empty(k_shape)
+        outs = q_out.data_ptr(), q_heads * dim, k_out.data_ptr(), kv_heads * dim
     else:
         q_out, k_out = out
+        outs = *_rows("q_out", q_out, q_shape, dtype, index), *_rows("k_out", k_out, k_shape, dtype, index)
     st = _lib.dq_qk_norm_rope(
         *_rows("q", q, q_shape, dtype, index), *_rows("k", k, k_shape, dtype, index), _dtype_code(q), tokens, q_heads,
         kv_heads, dim, *_weights(q_weight, k_weight, dim, index), epsilon,
         _arg("positions", positions, (tokens,), torch.int32, index),
         None if inv_freq is None else _arg("inv_freq", inv_freq, (half,), torch.float32, index), 2 * half,
-        1 if interleaved else 0, *_rows("q_out", q_out, q_shape, dtype, index),
-        *_rows("k_out", k_out, k_shape, dtype, index), _stream_of(index))
+        1 if interleaved else 0, *outs, _stream_of(index))
     if check and st != DQ_OK:
         raise DQError(st)
     return q_out, k_out
@@ -612,6 +616,9 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_
                                       q_weight, k_weight, epsilon, interleaved, out, None, check)
     if out is None:
         out = q.new_empty(q_shape)
+        outs = out.data_ptr(), q_heads * dim
+    else:
+        outs = _rows("out", out, q_shape, dtype, index)
     kc, vc, cdt, ks, vs, pages, page_size = _cache_args(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, index)
     st = _lib.dq_qk_norm_rope_cache(
         *_rows("q", q, q_shape, dtype, index), *_rows("k", k, k_shape, dtype, index),
@@ -619,7 +626,7 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, k_
         *_weights(q_weight, k_weight, dim, index), epsilon,
         _arg("positions", positions, (tokens,), torch.int32, index),
         None if inv_freq is None else _arg("inv_freq", inv_freq, (half,), torch.float32, index), 2 * half,
-        1 if interleaved else 0, *_rows("out", out, q_shape, dtype, index), kc, vc, cdt, ks, vs,
+        1 if interleaved else 0, *outs, kc, vc, cdt, ks, vs,
         _arg("slots", slots, (tokens,), torch.int64, index), pages, page_size, _stream_of(index))
     if check and st != DQ_OK:
         raise DQError(st)
@@ -659,6 +666,9 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale=None, v_sc
                                    sinks, out, lse, workspace, None, check)
     if out is None:
         out = q.new_empty(shape)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _arg("out", out, shape, dtype, index)
     kc, vc, cdt, ks, vs, pages, page_size = _cache_args(k_cache, v_cache, k_scale, v_scale, kv_heads, dim, dtype, index)
     if workspace is None:
         ws_bytes = _workspace_bytes(index, q_heads, kv_heads, dim, cdt)
@@ -674,7 +684,7 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, k_scale=None, v_sc
         _arg("page_table", page_table, (batch, max_pages), torch.int32, index),
         _arg("lengths", lengths, (batch,), torch.int32, index), batch, q_heads, kv_heads, dim, pages, page_size,
         max_pages, window, sinks, dim ** -0.5 if softmax_scale is None else softmax_scale,
-        _arg("out", out, shape, dtype, index),
+        out_ptr,
         None if lse is None else _arg("lse", lse, (batch, q_heads), torch.float32, index),
         None if workspace is None else workspace.data_ptr(), ws_bytes, _stream_of(index))
     if check and st != DQ_OK:
