@@ -181,7 +181,7 @@ KERNEL_SOURCES = {
                             "tma_pipeline.cuh", "ring_prefetch.cuh", "dq_args.cuh", "ada_launch.cu", "dq_launch.cuh"),
     "dequant_per_token": ("dequant_kernels.cuh", "dq_device.cuh", "dq_args.cuh", "dequant_launch.cu", "dq_launch.cuh"),
     "dequant_per_group": ("dequant_kernels.cuh", "dq_device.cuh", "dq_args.cuh", "dequant_launch.cu", "dq_launch.cuh"),
-    "w8a8_gemm": ("w8a8_gemm.cu", "tma_pipeline.cuh"),
+    "w8a8_gemm": ("w8a8_gemm.cu", "tcgen05_i8.cuh", "tensor_map.cuh", "tma_pipeline.cuh"),
 }
 
 
