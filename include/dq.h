@@ -394,7 +394,9 @@ dq_status dq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_
  *   k_cache, v_cache  device [num_pages, kv_heads, page_size, head_dim] of
  *                cache_dtype: `dtype`, or DQ_INT8 with the symmetric codes of
  *                dq_dynamic_quant over each head row (scale = absmax / 127,
- *                code = round(y / scale) of the binary32 row).
+ *                code = round(y / scale) of the binary32 row). A row with an
+ *                infinity or NaN has no codes: its scale is NaN, and
+ *                dq_paged_attention gives NaN wherever it is visible.
  *   k_scale, v_scale  device float [num_pages, kv_heads, page_size], required
  *                for DQ_INT8, otherwise ignored.
  *   v            device, like k (v_stride).

@@ -64,6 +64,25 @@ __device__ __forceinline__ float warp_sum_f32(float v) {
   return v;
 }
 
+// Maxima that a NaN passes through, for the magnitudes of a row that becomes codes:
+// the scale absmax / 127 of a row with a NaN is NaN (and so is that of a row with an
+// infinity), which the attention over the cache turns into NaN where it is visible.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <typename T>
 __device__ __forceinline__ T narrow(float v);
 template <>
@@ -154,10 +173,10 @@ __global__ void __launch_bounds__(kNormRopeBlock) norm_rope_generic_kernel(const
     if (CACHE == kCacheInt8 && which != 0) {
       float top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) top = fmaxf(top, fmaxf(fabsf(first[i]), fabsf(second[i])));
+      for (int i = 0; i < kPairs; ++i) top = max_nan(top, fabsf(first[i]), fabsf(second[i]));
 #pragma unroll
-      for (int i = 0; i < kRest; ++i) top = fmaxf(top, fabsf(rest[i]));
-      const RowQuant rq = make_sym<127>(warp_max(top));
+      for (int i = 0; i < kRest; ++i) top = max_nan(top, fabsf(rest[i]));
+      const RowQuant rq = make_sym<127>(warp_max_nan(top));
       const int64_t page = slot / a.page_size;
       const int64_t at = (page * a.kv_heads + h) * a.page_size + (slot - page * a.page_size);
       int8_t* y = static_cast<int8_t*>(which == 1 ? a.k_cache : a.v_cache) + at * a.head_dim;
@@ -386,6 +405,8 @@ __global__ void __launch_bounds__(kNormRopeBlock, kNormRopeCtas) norm_rope_kerne
   char* out = nullptr;
   int64_t out_step = 0, cache_row = 0;
   float2 w0[H], w1[H];
+#pragma unroll
+  for (int i = 0; i < H; ++i) w0[i] = w1[i] = f2(0.0f);  // lanes past the row: their zeros stay zeros
   const auto aim = [&]() {
     find(to);
     const int at = to.row - (to.which == 0 ? 0 : (to.which == 1 ? a.q_heads : normed_rows));
@@ -453,10 +474,10 @@ __global__ void __launch_bounds__(kNormRopeBlock, kNormRopeCtas) norm_rope_kerne
         float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < H; ++i)
-          top = max3(top, fmaxf(fabsf(f0[i].x), fabsf(f0[i].y)), fmaxf(fabsf(f1[i].x), fabsf(f1[i].y)));
+          top = max_nan(top, max_nan(fabsf(f0[i].x), fabsf(f0[i].y)), max_nan(fabsf(f1[i].x), fabsf(f1[i].y)));
 #pragma unroll
         for (int o = 1; o < (LANES ? LANES : 32); o *= 2) {
-          if (o < lanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (o < lanes) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
         }
         if (to.which != 0) {
           if (live) {
