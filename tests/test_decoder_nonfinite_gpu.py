@@ -63,3 +63,34 @@ def test_cache_scale_of_a_row_that_is_not_finite(dq, dim, rope_dim, dtype, what)
         out = dq.paged_attention(got_q[:2].contiguous(), *caches, table, lengths, *scales)
         assert out[0, 2 * head: 2 * head + 2].isnan().all()
         assert out[0, 2 - 2 * head: 4 - 2 * head].isfinite().all() and out[1].isfinite().all()
+
+
+@pytest.mark.parametrize("dim,rope_dim", [(128, 64), (64, 32), (96, 48), (256, 0), (128, 96), (20, 10)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_channels_past_the_rotation_stay_by_themselves(dq, dim, rope_dim, interleaved, what):
+    """An infinite input makes its own channel NaN (inf / inf) and the others 0; an infinite or NaN weight behind
+    the rotated channels touches its own channel only."""
+    q, k, _, pos, freq = rope_inputs(5, 3, 1, dim, BF16, rope_dim)
+    freq = freq if rope_dim else None
+    weight = torch.ones(dim, device="cuda")
+    clean = dq.qk_norm_rope(q, k, pos, freq, weight, weight, interleaved=interleaved)
+    for channel in (rope_dim, dim - 1, (rope_dim + dim) // 2):
+        w = weight.clone()
+        w[channel] = what
+        for got, want in zip(dq.qk_norm_rope(q, k, pos, freq, w, w, interleaved=interleaved), clean):
+            assert not got[..., channel].isfinite().any()
+            got, want = got.clone(), want.clone()
+            got[..., channel] = want[..., channel] = 0
+            assert torch.equal(got, want)
+        if what != math.inf:
+            continue
+        x, y = q.clone(), k.clone()
+        x[2, 1, channel], y[3, 0, channel] = what, -what
+        for (got, want), row in zip(zip(dq.qk_norm_rope(x, y, pos, freq, interleaved=interleaved), clean), ((2, 1), (3, 0))):
+            bad = torch.zeros(dim, dtype=torch.bool, device="cuda")
+            bad[channel] = True
+            assert got[row][bad].isnan().all() and (got[row][~bad] == 0).all()
+            got, want = got.clone(), want.clone()
+            got[row], want[row] = 0, 0
+            assert torch.equal(got, want)

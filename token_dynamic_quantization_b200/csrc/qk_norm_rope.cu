@@ -372,6 +372,9 @@ __global__ void __launch_bounds__(kNormRopeBlock, kNormRopeCtas) norm_rope_kerne
   // Angles: angle i turns channels (i, i + rope_dim / 2), or (2i, 2i + 1). The
   // lanes compute them once for the token's rows, then each picks its own VEC.
   float2 cs[H], sn[H], ns[H];
+  // chunks whose channels turn; the others are left out below, not turned by an angle of
+  // zero: an infinity would make its partner NaN
+  const bool turn0 = a.interleaved ? c0 < a.rope_dim : split, turn1 = a.interleaved ? c1 < a.rope_dim : split;
   if (half > 0) {
     const int32_t pos = a.positions[token];
     for (int i = lane; i < half; i += 32) rope_angle(pos, a.inv_freq[i], s_cos[warp][i], s_sin[warp][i]);
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kNormRopeBlock, kNormRopeCtas) norm_rope_kerne
   for (int i = 0; i < VEC; ++i) {
     // split: c0 + i; interleaved: c0 / 2 ... of the first chunk, then c1 / 2 ... of the second
     const int want = a.interleaved ? (i < H ? c0 / 2 + i : c1 / 2 + i - H) : c0 + i;
-    const bool turned = want < half && (a.interleaved || split);
+    const bool turned = i < H ? turn0 : turn1;
     const float c = turned ? s_cos[warp][want] : 1.0f, z = turned ? s_sin[warp][want] : 0.0f;
     if (i & 1) {
       cs[i / 2].y = c, sn[i / 2].y = z, ns[i / 2].y = -z;
@@ -455,10 +458,10 @@ __global__ void __launch_bounds__(kNormRopeBlock, kNormRopeCtas) norm_rope_kerne
           for (int i = 0; i < H; ++i) {
             const float ca = i & 1 ? cs[i / 2].y : cs[i / 2].x, sa = i & 1 ? sn[i / 2].y : sn[i / 2].x;
             const float cb = i & 1 ? cs[(H + i) / 2].y : cs[(H + i) / 2].x, sb = i & 1 ? sn[(H + i) / 2].y : sn[(H + i) / 2].x;
-            f0[i] = make_float2(f0[i].x * ca - f0[i].y * sa, f0[i].y * ca + f0[i].x * sa);
-            f1[i] = make_float2(f1[i].x * cb - f1[i].y * sb, f1[i].y * cb + f1[i].x * sb);
+            if (turn0) f0[i] = make_float2(f0[i].x * ca - f0[i].y * sa, f0[i].y * ca + f0[i].x * sa);
+            if (turn1) f1[i] = make_float2(f1[i].x * cb - f1[i].y * sb, f1[i].y * cb + f1[i].x * sb);
           }
-        } else {
+        } else if (turn0) {
 #pragma unroll
           for (int i = 0; i < H; ++i) {
             const float2 y0 = f0[i], y1 = f1[i];
