@@ -94,3 +94,29 @@ def test_channels_past_the_rotation_stay_by_themselves(dq, dim, rope_dim, interl
             got, want = got.clone(), want.clone()
             got[row], want[row] = 0, 0
             assert torch.equal(got, want)
+
+
+# tensor-core kernel with 64, 128 and 256 channels, with two sets of heads, and the scalar kernel (40)
+@pytest.mark.parametrize("dim,group", [(128, 4), (128, 12), (64, 4), (256, 2), (40, 2)])
+@pytest.mark.parametrize("page", [16, 5])
+@pytest.mark.parametrize("name", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+def test_scales_that_are_not_finite(dq, dim, group, page, name, what):
+    """NaN for the rows that see the token, whatever the signs of scores and codes and however small its weight."""
+    from test_paged_attention_gpu import call, make, verify
+
+    s = make([100, 700, 3], 2 * group, 2, dim, BF16, I8, page, seed=21)
+    clean = call(dq, s)
+    at = int(s["page_table"][1, 37 // page]), 1, 37 % page  # token 37 of sequence 1, key head 1
+    # weights from 1 down to nothing, for either sign of the token's scores
+    for scale in (dim**-0.5, 40.0, -40.0):
+        old = s[name][at].clone()
+        want = call(dq, s, softmax_scale=scale)
+        s[name][at] = what
+        got = call(dq, s, softmax_scale=scale)
+        assert got[1, group:].isnan().all()
+        assert torch.equal(got[[0, 2]], want[[0, 2]]) and torch.equal(got[1, :group], want[1, :group])
+        hidden = call(dq, s, window=600, sinks=4)
+        verify(s, hidden, window=600, sinks=4)
+        s[name][at] = old
+    assert torch.equal(call(dq, s), clean)

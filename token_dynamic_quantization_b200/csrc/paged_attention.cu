@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kPagedGenericWarps * 32) paged_attention_gener
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     float s = dot * to_log2;
-    if (kCodes) s *= a.k_scale[row];
+    if (kCodes) s = fmaf(s, a.k_scale[row], fmaf(a.k_scale[row], 0.0f, a.v_scale[row] * 0.0f));  // not finite: NaN
     const float next = fmaxf(m, s);
     const float keep = m == next ? 1.0f : exp2f(m - next);
     const float w = s == -INFINITY ? 0.0f : exp2f(s - next);

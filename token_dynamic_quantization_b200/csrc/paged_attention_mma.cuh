@@ -733,10 +733,12 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
             asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                          : "=f"(k_mul), "=f"(vw[mt][h])
                          : "r"(scales + st * Shape::kScaleBytes + tok * 8));
+            // NaN where a scale is not finite: such a token spoils the row whatever its weight
+            const float spoil = fmaf(k_mul, 0.0f, vw[mt][h] * 0.0f);
 #pragma unroll
             for (int ht = 0; ht < HT; ++ht) {
-              s[ht][mt][2 * h] *= k_mul;
-              s[ht][mt][2 * h + 1] *= k_mul;
+              s[ht][mt][2 * h] = fmaf(s[ht][mt][2 * h], k_mul, spoil);
+              s[ht][mt][2 * h + 1] = fmaf(s[ht][mt][2 * h + 1], k_mul, spoil);
             }
           }
           if (!inside) {
