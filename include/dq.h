@@ -457,8 +457,10 @@ dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, 
  * for DQ_F16, are exact, smaller ones within 0.5 / 16319 of it). Softmax statistics and
  * sums are binary32. A token's weight meets its value with 16 bits beside DQ_BF16
  * caches, with 11 beside DQ_F16 and DQ_INT8 caches; weights below 2^-30 of the
- * largest may count as zero. A scale (or, beside INT8 codes, a query) that is
- * infinite or NaN makes the rows that see it NaN.
+ * largest may count as zero. Beside INT8 codes that goes for the weight times the
+ * value scale, whose largest is taken for each query head by itself, so value scales may
+ * differ by anything (finite ones up to 2^120, those of finite bf16 values). A scale (or,
+ * beside INT8 codes, a query) that is infinite or NaN makes the rows that see it NaN.
  * 1 <= head_dim <= DQ_MAX_HEAD_DIM; q_heads a multiple of kv_heads, both <=
  * DQ_MAX_HEADS; 0 <= batch <= 65535 * 16, and 0 is a no-op; num_pages,
  * page_size, max_pages in [1, 2^31). Head dimensions 64, 128 and 256 with

@@ -22,20 +22,25 @@
 // a 16-bit integer (m16n8k32, exact int32 sums). O: a code's bits plus 128 in the low
 // byte of an f16 are a subnormal, (code + 128) * 2^-24, exact in the products; an
 // operand of 128s beside the same weights collects what the 128s add up to, and
-// it is taken off every other tile, while it is small. Value scales are folded into the weights,
-// relative to the power of two of the largest one so far, so weights keep f16's 11
-// bits whatever the scales' size. bf16 caches take their weights as a bf16 and what
+// it is taken off every other tile, while it is small. Value scales are folded into the
+// weights, relative to the power of two of a head's largest weight times scale so far (not
+// of the largest scale: its token may have no weight), so the products that count
+// keep f16's 11 bits whatever the scales' size. bf16 caches take their weights as a bf16 and what
 // it cuts off (16 bits): one bf16 alone would round each weight at 2^-9, as large an
 // error as the output's own rounding.
 //
-// The running maximum moves only when a score exceeds it by 8 (in log2): weights
-// then stay below 2^(8 + kLift) and the rescaling of O is rare. kLift raises
-// the weights in f16 so that those down to 2^-30 of the largest count.
+// The running maximum moves only when a score exceeds it by 8 (in log2), or beside
+// codes a weight times its scale may exceed f16's range: weights then stay below 2^(8 +
+// kLift) and the rescaling of O is rare. kLift raises the weights in f16 so that
+// those down to 2^-30 of the largest count.
+//
+// What a warp or a CTA leaves for others to join is its own quotient O / sum beside
+// (max, sum): no larger than the values, so that a join of large ones does not overflow.
 //
 // Work: all (sequence, key head, head set) items' tiles of TT tokens, laid end
 // to end, are cut into equal ranges, one per CTA, whatever the lengths; a CTA's
 // warps take its tiles in turn. Items inside one range are finished by their
-// CTA. Of an item that ranges cut, each CTA leaves (max, sum, O) in the
+// CTA. Of an item that ranges cut, each CTA leaves (max, sum, O / sum) in the
 // workspace, and a second kernel joins them. Short items (the host's rule) get a
 // CTA each and need no second kernel. Where there are many items (the host's
 // rule), a CTA is a single warp: no warp waits for another when an item ends.
@@ -67,7 +72,7 @@ struct PagedShape {
   static constexpr bool kCodes = sizeof(C) == 1;
   static constexpr int kTokens = kCodes && D <= 128 ? 32 : 16;
   static constexpr int kHeads = 8 * HT;
-  // one CTA's parts: O [kHeads][D], then (max, sum) [kHeads]
+  // one CTA's parts: O / sum [kHeads][D], then (max, sum) [kHeads]
   static constexpr int kPartFloats = kHeads * D + 2 * kHeads;
   // CTAs per SM: three, and two where their rings would be too short (codes of 128
   // channels: 109 us with two, 115 with three) or the registers do not allow more
@@ -154,6 +159,14 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// 1 / x of a sum of weights (0 for none): between 2^-126 and 2^126 a unit in the last place
+// off, and a sum of fewer than 2^31 weights stays there.
+__device__ __forceinline__ float inverse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return x == 0.0f ? 0.0f : r;
 }
 
 // A box of a tensor map, from element `x` of row `row` on, to `dst`.
@@ -625,12 +638,14 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 
     float o[HT][KS][4], m[HT][2], l[HT][2];
     float o_bias[HT][4];  // what the codes' bias of 128 has added to every channel of O
-    // the power of two that takes the value scales so far below 2, and the scale
-    // from which on it has to move
-    float v_mul = 1.0f, v_limit = 0x1p-149f;
-    bool v_first = true;
+    // the power of two that takes the head's largest weight times value scale so far
+    // into [1, 2)
+    float v_mul[HT][2];
+    // its reciprocal
+    const auto v_size = [&](int ht, int c) { return __uint_as_float((254u << 23) - __float_as_uint(v_mul[ht][c])); };
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
+      v_mul[ht][0] = v_mul[ht][1] = 0x1p126f;
       m[ht][0] = m[ht][1] = -INFINITY;
       l[ht][0] = l[ht][1] = 0.0f;
       o_bias[ht][0] = o_bias[ht][1] = o_bias[ht][2] = o_bias[ht][3] = 0.0f;
@@ -752,11 +767,10 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
           }
         }
       }
+      float v_top = 0.0f;
       if constexpr (kCodes) {
-        float top = fmaxf(fabsf(vw[0][0]), fabsf(vw[0][1]));
 #pragma unroll
-        for (int mt = 1; mt < MT; ++mt) top = max3(top, fabsf(vw[mt][0]), fabsf(vw[mt][1]));
-        move = top >= v_limit;
+        for (int mt = 0; mt < MT; ++mt) v_top = max3(v_top, fabsf(vw[mt][0]), fabsf(vw[mt][1]));
       }
 #pragma unroll
       for (int ht = 0; ht < HT; ++ht) {
@@ -766,6 +780,8 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 #pragma unroll
           for (int mt = 1; mt < MT; ++mt) top = max3(top, s[ht][mt][c], s[ht][mt][2 + c]);
           move |= top * q_mul[ht][c] > m[ht][c] + kSlack;
+          // none of the lane's operands below is larger than this
+          if constexpr (kCodes) move |= !(ex2(fmaf(top, q_mul[ht][c], kLift - m[ht][c])) * v_top * v_mul[ht][c] <= 0x1p15f);
         }
       }
       // hidden tokens of a group that was copied whole may hold anything: their
@@ -787,24 +803,8 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
           __syncwarp();
         }
       }
-      // ---- the running maximum and the largest value scale, when they have to move
+      // ---- the running maximum and the largest weight times scale, when they have to move
       if (__any_sync(0xffffffffu, move)) {
-        float v_keep = 1.0f;
-        if constexpr (kCodes) {
-          float top = 0.0f;
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) top = fmaxf(top, fmaxf(fabsf(vw[mt][0]), fabsf(vw[mt][1])));
-#pragma unroll
-          for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-          if (top >= v_limit) {
-            const uint32_t e = __float_as_uint(top) >> 23;  // 2^(127 - e) takes top into [1, 2)
-            const float next = __uint_as_float((254u - (e < 1u ? 1u : (e > 253u ? 253u : e))) << 23);
-            v_keep = v_first ? 0.0f : next / v_mul;  // nothing but zeros so far: O is 0
-            v_first = false;
-            v_mul = next;
-            v_limit = 2.0f / next;
-          }
-        }
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
@@ -815,13 +815,29 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             top *= q_mul[ht][c];
-            float keep = 1.0f;
+            float fall = 0.0f;  // log2 of what the weights so far are multiplied by
             if (top > m[ht][c]) {
-              keep = exp2f(m[ht][c] - top);
+              fall = m[ht][c] - top;
               m[ht][c] = top;
-              l[ht][c] *= keep;
+              l[ht][c] *= exp2f(fall);
             }
-            keep *= v_keep;
+            if constexpr (kCodes) {
+              float x = 0.0f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  x = fmaxf(x, ex2(fmaf(s[ht][mt][2 * h + c], q_mul[ht][c], -m[ht][c])) * fabsf(vw[mt][h]));
+              }
+#pragma unroll
+              for (int y = 4; y < 32; y *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+              x = fmaxf(x, exp2f(fall) * v_size(ht, c));
+              const uint32_t e = __float_as_uint(x) >> 23;  // 2^(127 - e) takes x into [1, 2)
+              const uint32_t next = 254u - (e < 1u ? 1u : (e > 253u ? 253u : e));
+              fall += static_cast<float>(static_cast<int>(next) - static_cast<int>(__float_as_uint(v_mul[ht][c]) >> 23));
+              v_mul[ht][c] = __uint_as_float(next << 23);
+            }
+            const float keep = exp2f(fall);
             o_bias[ht][c] *= keep;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
@@ -851,9 +867,8 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
             l[ht][0] += w0;
             l[ht][1] += w1;
             if constexpr (kCodes) {
-              const float f = vw[mt][h] * v_mul;
-              w0 *= f;
-              w1 *= f;
+              w0 = w0 * vw[mt][h] * v_mul[ht][0];
+              w1 = w1 * vw[mt][h] * v_mul[ht][1];
             }
             if constexpr (kBf16) {
               const uint32_t hi = pack_bf16(w0, w1);
@@ -944,7 +959,6 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 
     if (kCodes && biased) remove_bias();
     // ---- join the warps
-    const float v_undo = (kCodes ? 0x1p24f : 1.0f) / v_mul;
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
@@ -957,13 +971,15 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
           s_stat[(warp * kHeads + h) * 2] = m[ht][c];
           s_stat[(warp * kHeads + h) * 2 + 1] = sum;
         }
+        // codes: 2^24 / v_mul in two factors, either of which is finite
+        const float inv = (kCodes ? 0x1p24f : 1.0f) * inverse(sum), size = kCodes ? v_size(ht, c) : 1.0f;
         // row tile i holds the lane's channels 2i and 2i + 1, counted over its V pieces
         float* dst = s_o + (warp * kHeads + h) * Shape::kPitch + kVPiece * g;
 #pragma unroll
         for (int i = 0; i < KS; i += 2) {
           const int ch = (2 * i / kVPiece) * 8 * kVPiece + 2 * i % kVPiece;
-          *reinterpret_cast<float4*>(dst + ch) = make_float4(o[ht][i][c] * v_undo, o[ht][i][2 + c] * v_undo,
-                                                             o[ht][i + 1][c] * v_undo, o[ht][i + 1][2 + c] * v_undo);
+          *reinterpret_cast<float4*>(dst + ch) = make_float4(o[ht][i][c] * inv * size, o[ht][i][2 + c] * inv * size,
+                                                             o[ht][i + 1][c] * inv * size, o[ht][i + 1][2 + c] * inv * size);
         }
       }
     }
@@ -987,12 +1003,18 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
       float top = -INFINITY, total = 0.0f;
 #pragma unroll
       for (int w = 0; w < W; ++w) top = fmaxf(top, s_stat[(w * kHeads + h) * 2]);
-      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float share[W];
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const float mw = s_stat[(w * kHeads + h) * 2];
-        const float f = mw == top ? 1.0f : exp2f(mw - top);
-        total = fmaf(s_stat[(w * kHeads + h) * 2 + 1], f, total);
+        share[w] = s_stat[(w * kHeads + h) * 2 + 1] * (mw == top ? 1.0f : exp2f(mw - top));
+        total += share[w];
+      }
+      const float inv = inverse(total);
+      float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = share[w] * inv;
         const float4 v = *reinterpret_cast<const float4*>(s_o + (w * kHeads + h) * Shape::kPitch + c);
         sum.x = fmaf(v.x, f, sum.x);
         sum.y = fmaf(v.y, f, sum.y);
@@ -1001,8 +1023,8 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
       }
       if (complete) {
         const int64_t at = done_seq * a.q_heads + done_head0 + h;
-        const float r = empty ? 0.0f : 1.0f / total;
-        store_row4(static_cast<T*>(a.out) + at * D + c, sum, r);
+        // no weight at all, though tokens are visible: 0 / 0
+        store_row4(static_cast<T*>(a.out) + at * D + c, sum, total == 0.0f && !empty ? NAN : 1.0f);
         if (a.lse != nullptr && c == 0)
           a.lse[at] = empty ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
       } else {
@@ -1071,13 +1093,19 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel
       float next = top;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) next = fmaxf(next, st[i].x);
-      const float keep = top == next ? 1.0f : exp2f(top - next);
-      sum_l *= keep;
+      const float before = sum_l * (top == next ? 1.0f : exp2f(top - next));
+      float share[kBatch];
+      sum_l = before;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        share[i] = st[i].y * (st[i].x == next ? 1.0f : exp2f(st[i].x - next));
+        sum_l += share[i];
+      }
+      const float inv = inverse(sum_l), keep = before * inv;
       sum.x *= keep, sum.y *= keep, sum.z *= keep, sum.w *= keep;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float f = st[i].x == next ? 1.0f : exp2f(st[i].x - next);
-        sum_l = fmaf(st[i].y, f, sum_l);
+        const float f = share[i] * inv;
         sum.x = fmaf(v[i].x, f, sum.x);
         sum.y = fmaf(v[i].y, f, sum.y);
         sum.z = fmaf(v[i].z, f, sum.z);
@@ -1096,11 +1124,12 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel
     if (split == 0) {
       for (int p = row + mine; p < splits * mine; p += mine) top = fmaxf(top, s_m[p]);
       sum_l = 0.0f;
+      for (int p = row; p < splits * mine; p += mine) sum_l = fmaf(s_l[p], s_m[p] == top ? 1.0f : exp2f(s_m[p] - top), sum_l);
+      const float inv = inverse(sum_l);
       sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int p = row; p < splits * mine; p += mine) {
-        const float f = s_m[p] == top ? 1.0f : exp2f(s_m[p] - top);
+        const float f = s_l[p] * (s_m[p] == top ? 1.0f : exp2f(s_m[p] - top)) * inv;
         const float4 v = *reinterpret_cast<const float4*>(&s_o[p][4 * vec]);
-        sum_l = fmaf(s_l[p], f, sum_l);
         sum.x = fmaf(v.x, f, sum.x);
         sum.y = fmaf(v.y, f, sum.y);
         sum.z = fmaf(v.z, f, sum.z);
@@ -1110,7 +1139,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel
   }
   if (split == 0) {
     const int64_t at = cut.seq * a.q_heads + kvh * a.group + set * kHeads + h;
-    store_row4(static_cast<T*>(a.out) + at * D + 4 * vec, sum, 1.0f / sum_l);
+    store_row4(static_cast<T*>(a.out) + at * D + 4 * vec, sum, sum_l == 0.0f ? NAN : 1.0f);
     if (vec == 0 && a.lse != nullptr) a.lse[at] = ((top == -INFINITY ? 0.0f : top) - kLift + log2f(sum_l)) * kLn2;
   }
 }
