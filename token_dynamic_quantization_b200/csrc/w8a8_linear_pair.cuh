@@ -324,6 +324,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         for (uint32_t j = slice > kPairStages ? slice - kPairStages : 0; j < slice; ++j)
           mbar_wait_parity(full + j % kPairStages, (j / kPairStages) & 1u);
       }
+      // nor an arrival of the leader's commits that frees a stage
+      for (uint32_t j = slice > kPairStages ? slice - kPairStages : 0; ok && j < slice; ++j)
+        ok = wait_or_abort_for(empty + j % kPairStages, (j / kPairStages) & 1u, abort_flag, kWaitLimitNs);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -359,9 +362,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         if (ok) tc_commit_pair(acc_full + acc);
       }
-      // the TMEM is freed below: every MMA issued has completed first
+      // both CTAs wait for it below: the TMEM is freed, and a CTA's barriers go, only after
+      // every MMA issued has completed
       tc_commit_pair(mma_done);
-      mbar_wait_parity(mma_done, 0);
     }
     __syncwarp();
   } else {
@@ -464,6 +467,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // the last commit arrives in both CTAs; every accumulator it stands for has been read by now
+  if (threadIdx.x == 32) mbar_wait_parity(mma_done, 0);
+  __syncwarp();
   cluster_barrier();  // no CTA leaves (or frees TMEM) while its peer still uses it
   if (warp == 1) {
     tc_fence_after();
