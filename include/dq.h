@@ -456,7 +456,8 @@ dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, 
  * the largest channel of its head (channels within 2^-7 of it for DQ_BF16, 2^-4
  * for DQ_F16, are exact, smaller ones within 0.5 / 16319 of it). Softmax statistics and
  * sums are binary32. A token's weight meets its value with 16 bits beside DQ_BF16
- * caches, with 11 beside DQ_F16 and DQ_INT8 caches; weights below 2^-30 of the
+ * caches, with 11 beside DQ_INT8 caches where the output is DQ_BF16 (whose half step is
+ * eight times a weight's), else with 20; weights below 2^-30 of the
  * largest may count as zero. Beside INT8 codes that goes for the weight times the
  * value scale, whose largest is taken for each query head by itself, so value scales may
  * differ by anything (finite ones up to 2^120, those of finite bf16 values). A scale (or,

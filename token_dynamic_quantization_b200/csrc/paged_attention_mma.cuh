@@ -25,9 +25,15 @@
 // it is taken off every other tile, while it is small. Value scales are folded into the
 // weights, relative to the power of two of a head's largest weight times scale so far (not
 // of the largest scale: its token may have no weight), so the products that count
-// keep f16's 11 bits whatever the scales' size. bf16 caches take their weights as a bf16 and what
-// it cuts off (16 bits): one bf16 alone would round each weight at 2^-9, as large an
-// error as the output's own rounding.
+// keep f16's bits whatever the scales' size.
+//
+// A weight is rounded to 16 bits for its product, and what that cuts off goes into a
+// second one: alone, a bf16 would be off by 2^-9 beside bf16 outputs, an f16 by 2^-12 beside f16
+// outputs, as much as the output's own rounding (f16 caches: 2.8e-4 of the result in
+// norm against 2.1e-4). Beside codes with bf16 outputs one f16 is enough, an eighth of the
+// output's half step; there the second would cost 3 % with up to 8 query heads to a
+// key head (64 x 8192: 112 us from 108.4) and 10 % with more (64 x 4000, 16 heads: 97.6 us
+// from 88.8). Beside f16 it costs 1 to 5 % (window 48 x 6000: 30.4 us from 28.9).
 //
 // The running maximum moves only when a score exceeds it by 8 (in log2), or beside
 // codes a weight times its scale may exceed f16's range: weights then stay below 2^(8 +
@@ -341,6 +347,8 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
   constexpr int kItemCost = dq::kItemCost<W>;
   constexpr bool kCodes = Shape::kCodes;
   constexpr bool kBf16 = !kCodes && sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
+  // a weight as two operands of 16 bits; one of f16 does beside codes where the output is bf16
+  constexpr bool kTwoParts = !kCodes || __is_same(T, __half);
   constexpr int TT = Shape::kTokens, MT = TT / 16, kHeads = Shape::kHeads;
   constexpr int kElem = sizeof(C);
   constexpr int kPiece = 16 / kElem;         // elements of a 16-byte piece
@@ -870,13 +878,18 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
               w0 = w0 * vw[mt][h] * v_mul[ht][0];
               w1 = w1 * vw[mt][h] * v_mul[ht][1];
             }
+            // what 16 bits cut off, kept in a second operand
             if constexpr (kBf16) {
               const uint32_t hi = pack_bf16(w0, w1);
               p[ht][mt][h] = movmatrix(hi);
-              // what bf16 cuts off, kept in a second operand: 16 bits of weight
               p_lo[ht][mt][h] = movmatrix(pack_bf16(w0 - __uint_as_float(hi << 16), w1 - __uint_as_float(hi & 0xFFFF0000u)));
             } else {
-              p[ht][mt][h] = movmatrix(pack_f16(w0, w1));
+              const uint32_t hi = pack_f16(w0, w1);
+              p[ht][mt][h] = movmatrix(hi);
+              if constexpr (kTwoParts) {
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                p_lo[ht][mt][h] = movmatrix(pack_f16(w0 - back.x, w1 - back.y));
+              }
             }
           }
         }
@@ -906,6 +919,12 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
                                 bytes_f16(cd01, 0x4140u), bytes_f16(cd01, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
                 mma16816<false>(o[ht][tile0 + 1], bytes_f16(ab23, 0x4140u), bytes_f16(ab23, 0x4342u),
                                 bytes_f16(cd23, 0x4140u), bytes_f16(cd23, 0x4342u), p[ht][mt][0], p[ht][mt][1]);
+                if constexpr (kTwoParts) {
+                  mma16816<false>(o[ht][tile0], bytes_f16(ab01, 0x4140u), bytes_f16(ab01, 0x4342u),
+                                  bytes_f16(cd01, 0x4140u), bytes_f16(cd01, 0x4342u), p_lo[ht][mt][0], p_lo[ht][mt][1]);
+                  mma16816<false>(o[ht][tile0 + 1], bytes_f16(ab23, 0x4140u), bytes_f16(ab23, 0x4342u),
+                                  bytes_f16(cd23, 0x4140u), bytes_f16(cd23, 0x4342u), p_lo[ht][mt][0], p_lo[ht][mt][1]);
+                }
               }
             } else {  // two channels of two token pairs: one row tile
               const int tile0 = i * (kVBytes / 4) + w;
@@ -914,7 +933,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 #pragma unroll
               for (int ht = 0; ht < HT; ++ht) {
                 mma16816<kBf16>(o[ht][tile0], a0, a1, a2, a3, p[ht][mt][0], p[ht][mt][1]);
-                if constexpr (kBf16)
+                if constexpr (kTwoParts)
                   mma16816<kBf16>(o[ht][tile0], a0, a1, a2, a3, p_lo[ht][mt][0], p_lo[ht][mt][1]);
               }
             }
@@ -927,8 +946,11 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 #pragma unroll
         for (int ht = 0; ht < HT; ++ht) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int mt = 0; mt < MT; ++mt) {
             mma16816<false>(o_bias[ht], 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, p[ht][mt][0], p[ht][mt][1]);
+            if constexpr (kTwoParts)
+              mma16816<false>(o_bias[ht], 0x00800080u, 0x00800080u, 0x00800080u, 0x00800080u, p_lo[ht][mt][0], p_lo[ht][mt][1]);
+          }
         }
         biased = !biased;
         if (!biased) remove_bias();
