@@ -325,8 +325,10 @@ typedef enum dq_activation {
  *   out[m,n] = t[m,n] rounded to out_dtype
  * The integer sum is exact; everything after it is binary32, the products and
  * sums rounded once in that order (without an activation the result is
- * therefore bit-identical to the formula); the activations' exponentials and
- * error function are accurate to a few units in the last place of binary32.
+ * therefore bit-identical to the formula). The error of an activation grows with
+ * the size of its exponential's argument, which is binary32: relative to the value, at
+ * most (x^2 + 8) 2^-22 for GELU and (|u| + 8) 2^-22 for SILU (u = x) and GELU_TANH (u =
+ * 2 sqrt(2 / pi) (x + 0.044715 x^3)), x / (1 + exp(-u)). Values below 2^-119 may be zero.
  * Arguments: a, b, m, n, k, a_scale, b_scale as in dq_w8a8_gemm;
  *   bias        device [n] of bias_dtype (DQ_F32, DQ_F16, DQ_BF16) or NULL
  *               (bias_dtype then ignored).

@@ -36,14 +36,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return r;
 }
 
-// The activations, a few units in the last place of binary32 (the argument of
-// an exponential is rounded: |u| 2^-24 of the result), at a cost that the
-// epilogue hides: on 4096^3 with bias and residual 128 values per thread and
-// tile share the issue slots of 16384 tensor-core cycles.
+// The activations at a cost that the epilogue hides: on 4096^3 with bias and
+// residual 128 values per thread and tile share the issue slots of 16384
+// tensor-core cycles. The argument of an exponential is rounded, which costs |u| 2^-24 of
+// the result (GELU: x^2 2^-24): next to zero a few units in the last place of
+// binary32, 17 at GELU(-6) and 63 at GELU(-12). A quotient whose denominator passes 2^126
+// is zero (SILU from -87.3 on, whose value there is 2^-119).
 //   GELU  x Phi(x). With z = |x| / sqrt 2 and t = 1 / (1 + z / 2),
 //         erfc(z) / 2 = t 2^(-z^2 log2(e) + Q(t)); Q is a degree-9 minimax fit of
-//         log2(erfcx(z) / (2 t)) on 0 <= z <= 10.5 (5e-8; beyond, the result
-//         has underflowed), so negative tails keep their relative accuracy.
+//         log2(erfcx(z) / (2 t)) on 0 <= z <= 10.5 (within 1.8e-7; beyond, the
+//         result has underflowed), so negative tails keep their relative accuracy.
 //   GELU_TANH, SILU  x / (1 + exp(-u)) with u = 2 sqrt(2/pi) (x + 0.044715 x^3), or x.
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
