@@ -12,6 +12,7 @@
 // window leaves behind the first tokens.
 #include <cmath>
 
+#include "decoder_launch.cuh"
 #include "dq.h"
 #include "dq_device.cuh"
 #include "dq_launch.cuh"
@@ -154,25 +155,6 @@ bool rows_map(CUtensorMap* map, const void* base, int64_t rows, int dim, int box
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Kernel, typename... Args>
-dq_status launch_pdl(Kernel kernel, dim3 grid, int block, size_t smem, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return DQ_ERR_CUDA;
-  }
-  return dq_host::launch_status();
-}
-
 template <typename T, typename C, int D, int HT, bool RUN, int W>
 dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
   using Shape = dq::PagedShape<C, D, HT, W>;
@@ -189,14 +171,14 @@ dq_status launch_mma(dq::PagedArgs a, cudaStream_t stream) {
   if (ctas > most_ctas()) ctas = most_ctas();
   if (a.whole) {
     const dim3 items(static_cast<unsigned>(a.batch * a.kv_heads * a.head_sets));
-    return launch_pdl(fn, items, Shape::kThreads, Shape::kSmem, stream, k_map, v_map, a);
+    return dq_host::launch_dependent(fn, items, Shape::kThreads, Shape::kSmem, 1, stream, k_map, v_map, a);
   }
   a.cuts = reinterpret_cast<dq::PagedCut*>(a.parts + most_ctas() * 2 * Shape::kPartFloats);
   const dim3 grid(static_cast<unsigned>(ctas));
-  const dq_status st = launch_pdl(fn, grid, Shape::kThreads, Shape::kSmem, stream, k_map, v_map, a);
+  const dq_status st = dq_host::launch_dependent(fn, grid, Shape::kThreads, Shape::kSmem, 1, stream, k_map, v_map, a);
   if (st != DQ_OK) return st;
-  return launch_pdl(dq::paged_attention_join_kernel<T, C, D, HT>, dim3(static_cast<unsigned>(ctas - 1)),
-                    dq::kPagedJoinThreads, 0, stream, a);
+  return dq_host::launch_dependent(dq::paged_attention_join_kernel<T, C, D, HT>, dim3(static_cast<unsigned>(ctas - 1)),
+                                   dq::kPagedJoinThreads, 0, 1, stream, a);
 }
 
 // How the work is cut, from the number of items (sequence, key head, head set)

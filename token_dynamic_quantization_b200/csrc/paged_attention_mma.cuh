@@ -61,6 +61,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "decoder_device.cuh"
 #include "dq_device.cuh"
 #include "paged_attention_args.cuh"
 #include "tma_pipeline.cuh"
@@ -143,13 +144,6 @@ __device__ __forceinline__ void store_row4(T* out, const float4& v, float r) {
   }
 }
 
-__device__ __forceinline__ void mma16832_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                            uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 // The value of 16 bits of type T.
 template <typename T>
 __device__ __forceinline__ float half_bits(uint32_t b) {
@@ -161,18 +155,10 @@ __device__ __forceinline__ float half_bits(uint32_t b) {
 // 2^-24, exact in the products.
 __device__ __forceinline__ uint32_t bytes_f16(uint32_t w, uint32_t sel) { return prmt(w, 0u, sel); }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // 1 / x of a sum of weights (0 for none): between 2^-126 and 2^126 a unit in the last place
 // off, and a sum of fewer than 2^31 weights stays there.
 __device__ __forceinline__ float inverse(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return x == 0.0f ? 0.0f : r;
+  return x == 0.0f ? 0.0f : rcp_approx(x);
 }
 
 // A box of a tensor map, from element `x` of row `row` on, to `dst`.
@@ -201,15 +187,6 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int BYTES>
-__device__ __forceinline__ void load_piece(uint32_t (&r)[BYTES / 4], uint32_t addr) {
-  if constexpr (BYTES == 16) {
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
-  } else {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
-  }
 }
 
 // Offset of 16-byte piece `piece` of row `row` in a stage's boxes, as the
@@ -709,7 +686,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
               for (int i = 0; i < KP; ++i) {
 #pragma unroll
                 for (int u = 0; u < 4; u += 2)
-                  mma16832_s8(d, k0[i][u], k1[i][u], k0[i][u + 1], k1[i][u + 1], qf[ht][4 * i + u][digit],
+                  mma_s8(d, k0[i][u], k1[i][u], k0[i][u + 1], k1[i][u + 1], qf[ht][4 * i + u][digit],
                               qf[ht][4 * i + u + 1][digit]);
               }
             }
@@ -789,7 +766,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
           for (int mt = 1; mt < MT; ++mt) top = max3(top, s[ht][mt][c], s[ht][mt][2 + c]);
           move |= top * q_mul[ht][c] > m[ht][c] + kSlack;
           // none of the lane's operands below is larger than this
-          if constexpr (kCodes) move |= !(ex2(fmaf(top, q_mul[ht][c], kLift - m[ht][c])) * v_top * v_mul[ht][c] <= 0x1p15f);
+          if constexpr (kCodes) move |= !(exp2_approx(fmaf(top, q_mul[ht][c], kLift - m[ht][c])) * v_top * v_mul[ht][c] <= 0x1p15f);
         }
       }
       // hidden tokens of a group that was copied whole may hold anything: their
@@ -835,7 +812,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
               for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                  x = fmaxf(x, ex2(fmaf(s[ht][mt][2 * h + c], q_mul[ht][c], -m[ht][c])) * fabsf(vw[mt][h]));
+                  x = fmaxf(x, exp2_approx(fmaf(s[ht][mt][2 * h + c], q_mul[ht][c], -m[ht][c])) * fabsf(vw[mt][h]));
               }
 #pragma unroll
               for (int y = 4; y < 32; y *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
@@ -865,7 +842,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
         for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float w0 = ex2(fmaf(s[ht][mt][2 * h], q_mul[ht][0], -z0)), w1 = ex2(fmaf(s[ht][mt][2 * h + 1], q_mul[ht][1], -z1));
+            float w0 = exp2_approx(fmaf(s[ht][mt][2 * h], q_mul[ht][0], -z0)), w1 = exp2_approx(fmaf(s[ht][mt][2 * h + 1], q_mul[ht][1], -z1));
             if (!inside) {  // a factor of zero takes a hidden token's -infinity to NaN
               bool seen;
               token_of(tl, 16 * mt + 8 * h + order, seen);

@@ -5,6 +5,7 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "decoder_device.cuh"
 #include "dq.h"
 #include "dq_device.cuh"
 
@@ -24,17 +25,6 @@ struct LinearArgs {
   int vec_out;   // rows of out (and residual) start 16-byte aligned
   int pair_out;  // two neighbouring even columns lie in one aligned access, in every row
 };
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // The activations at a cost that the epilogue hides: on 4096^3 with bias and
 // residual 128 values per thread and tile share the issue slots of 16384

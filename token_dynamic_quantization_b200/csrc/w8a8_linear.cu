@@ -2,6 +2,7 @@
 // (dq_w8a8_linear).
 #include <atomic>
 
+#include "decoder_launch.cuh"
 #include "dq.h"
 #include "dq_launch.cuh"
 #include "w8a8_epilogue.cuh"
@@ -98,30 +99,6 @@ int best_split(int64_t tiles, int64_t pieces, const int* resident) {
   return split;
 }
 
-// A programmatic dependent launch in clusters of `cluster` CTAs along x.
-template <typename Kernel, typename... Args>
-dq_status launch_cluster(Kernel kernel, dim3 grid, int block, size_t smem, int cluster, cudaStream_t stream, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
-    cudaGetLastError();
-    return DQ_ERR_CUDA;
-  }
-  return dq_host::launch_status();
-}
-
 // Up to 8 tokens: a CTA for every 16 weight rows.
 template <int ACT>
 dq_status launch_few(const dq::LinearArgs& a, cudaStream_t stream) {
@@ -149,7 +126,7 @@ dq_status launch_split(const dq::LinearArgs& a, cudaStream_t stream) {
   if (device < 0 || device >= dq_host::kMaxDevices) return dq_host::kNotLaunchable;
   const int split = best_split(blocks, (a.k + 127) / 128,
                                resident_clusters(fn, device, dq::kSplitThreads, Shape::kSmem, known[device], resident));
-  return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * split)), dq::kSplitThreads, Shape::kSmem, split, stream, w,
+  return dq_host::launch_dependent(fn, dim3(static_cast<unsigned>(blocks * split)), dq::kSplitThreads, Shape::kSmem, split, stream, w,
                         x, a, split);
 }
 
@@ -171,7 +148,7 @@ dq_status launch_pair(const dq::LinearArgs& a, cudaStream_t stream) {
   ps.wide = tiles - split;
   ps.items = tiles + split;
   const int64_t clusters = ps.items < pairs ? ps.items : pairs;
-  return launch_cluster(fn, dim3(static_cast<unsigned>(2 * clusters)), dq::kPairThreads, dq::PairShape<TURN>::kSmem, 1, stream, ma,
+  return dq_host::launch_dependent(fn, dim3(static_cast<unsigned>(2 * clusters)), dq::kPairThreads, dq::PairShape<TURN>::kSmem, 1, stream, ma,
                         mb128, mb64, a, ps);
 }
 

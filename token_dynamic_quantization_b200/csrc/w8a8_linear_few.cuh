@@ -16,6 +16,7 @@
 // three stages of 512. Every wait is bounded; a sum that misses a copy becomes NaN.
 #pragma once
 
+#include "decoder_device.cuh"
 #include "dq_launch.cuh"
 #include "tma_pipeline.cuh"
 #include "w8a8_epilogue.cuh"
@@ -34,19 +35,6 @@ constexpr int kFewTokenStage = kFewTokens * kFewTokenPitch;
 constexpr int kFewSumPitch = kFewRows + 4;                // int32 parts [warp][token][row]
 constexpr int kFewBody = kFewWarps * kFewStages * kFewStage + 2 * kFewTokenStage;
 constexpr size_t kFewSmem = size_t(kFewBody) + kFewTokens * 4 + kFewWarps * kFewStages * 8 + 16;
-
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint4 load_piece16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-  return v;
-}
 
 template <int ACT>
 __global__ void __launch_bounds__(kFewThreads) w8a8_linear_few_kernel(const LinearArgs a) {
@@ -138,10 +126,12 @@ __global__ void __launch_bounds__(kFewThreads) w8a8_linear_few_kernel(const Line
 #pragma unroll
       for (int s = 0; s < kFewRun / 64; ++s) {
         if (64 * s < bytes) {
-          const uint4 x0 = load_piece16(wx + 64 * s), x1 = load_piece16(wx + 8 * kFewRowPitch + 64 * s);
-          const uint4 y = load_piece16(tx + 64 * s);
-          mma_s8(acc, x0.x, x1.x, x0.y, x1.y, y.x, y.y);
-          mma_s8(acc, x0.z, x1.z, x0.w, x1.w, y.z, y.w);
+          uint32_t x0[4], x1[4], y[4];
+          load_piece<16>(x0, wx + 64 * s);
+          load_piece<16>(x1, wx + 8 * kFewRowPitch + 64 * s);
+          load_piece<16>(y, tx + 64 * s);
+          mma_s8(acc, x0[0], x1[0], x0[1], x1[1], y[0], y[1]);
+          mma_s8(acc, x0[2], x1[2], x0[3], x1[3], y[2], y[3]);
         }
       }
       __syncwarp();
