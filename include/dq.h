@@ -27,7 +27,8 @@
  *                           (dq_qk_norm_rope_cache: keys and values go
  *                           straight into a paged 16-bit or INT8 cache).
  *   dq_paged_attention      attention of one new token per sequence over
- *                           that cache, split over its length and joined.
+ *                           that cache; for 64, 128 and 256 channels split
+ *                           over its length and joined.
  *
  * plus the workspace queries of the two-phase calling convention both pages
  * describe ("...GetWorkspaceSize" first, then the run): dq_get_workspace_size,
@@ -341,7 +342,8 @@ typedef enum dq_activation {
  * rows and K, not by tokens; the parts are exact integers, so a token's result
  * depends neither on the split nor on the other tokens. k a multiple of 16 with
  * 16-byte aligned a and b runs on the tensor cores, anything else a CUDA-core
- * kernel with the same result but for the activations' last places.
+ * kernel with the same result but for the activations' last places, and slow (1 x
+ * 4096 x 1000: 52 us; 512 x 1024 x 1000: 0.7 ms, with k = 1008 9 us).
  * Errors: as dq_w8a8_gemm (DQ_ERR_BAD_ARGUMENT for an unknown activation). */
 dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m, int64_t n, int64_t k,
                          const float* a_scale, const float* b_scale, const void* bias, dq_dtype bias_dtype,
@@ -361,8 +363,9 @@ dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m, int64_t n,
  *   (y[a], y[b]) <- (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
  * with (a, b) = (i, i + rope_dim / 2), or (2i, 2i + 1) when interleaved;
  * channels from rope_dim on are normed only. Norm and rotation are binary32,
- * rounded once into the output; the angle is reduced in binary64, so far
- * positions keep their accuracy (any int32 position is valid).
+ * rounded once into the output; the angle is reduced as an exact product of the
+ * position and a 64-bit fraction of a turn, so far positions keep their
+ * accuracy (any int32 position is valid).
  * Arguments
  *   q, k         device, token t's heads at q + t * q_stride (elements), head
  *                h of it at + h * head_dim: slices of one fused projection
@@ -377,7 +380,8 @@ dq_status dq_w8a8_linear(const int8_t* a, const int8_t* b, int64_t m, int64_t n,
  *   rope_dim     even, 0 <= rope_dim <= head_dim.
  *   interleaved  0 or 1.
  *   q_out, k_out device, strided as q and k are. q_out may be q itself with
- *                the same stride, k_out may be k likewise.
+ *                the same stride, k_out may be k likewise; they must not
+ *                overlap an input or each other in any other way.
  * 1 <= head_dim <= DQ_MAX_HEAD_DIM; 1 <= q_heads, kv_heads <= DQ_MAX_HEADS;
  * 0 <= tokens < 2^31, and 0 is a no-op. Rows of 16-byte aligned vectors take
  * a vectorised path; others a scalar one, with the same formula. A row's
@@ -467,9 +471,17 @@ dq_status dq_paged_attention_get_workspace_size(int64_t batch, int32_t q_heads, 
  * 1 <= head_dim <= DQ_MAX_HEAD_DIM; q_heads a multiple of kv_heads, both <=
  * DQ_MAX_HEADS; 0 <= batch <= 65535 * 16, and 0 is a no-op; num_pages,
  * page_size, max_pages in [1, 2^31). Head dimensions 64, 128 and 256 with
- * 16-byte aligned tensors run on the tensor cores; others run a CUDA-core
- * kernel (binary32 weights). Pages of a multiple of 16 tokens are copied in
- * boxes, others row by row, which takes about a tenth longer.
+ * 16-byte aligned tensors run on the tensor cores. Others run a CUDA-core
+ * kernel (binary32 weights) that is right for all but slow: a CTA per sequence
+ * and query head reads the key head's rows for itself and takes the whole length
+ * (64 sequences of up to 4000 tokens, INT8, 32 query and 8 key heads: 2.0 ms with
+ * 80 or 96 channels, 64 us with 128; one of 32768 with 80: 13 ms).
+ * On the tensor cores one pass over a key head's rows serves 16 query heads (8
+ * with 256 channels); more read them again. Pages of a multiple of 16 tokens
+ * are copied in boxes, others row by row, which takes about a tenth longer. How
+ * the work is cut goes by max_pages: for short sequences a page table no wider than
+ * they need is faster (up to 256 tokens in all; beside INT8 codes and up to 128
+ * channels 512).
  * Errors: as dq_qk_norm_rope, DQ_ERR_WORKSPACE_TOO_SMALL. */
 dq_status dq_paged_attention(const void* q, dq_dtype q_dtype, int64_t q_stride, const void* k_cache,
                              const void* v_cache, dq_dtype cache_dtype, const float* k_scale, const float* v_scale,

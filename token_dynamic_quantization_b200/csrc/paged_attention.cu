@@ -8,7 +8,9 @@
 // so the cache is read once, and parts of a sequence that were computed apart
 // join by the same rule. Head dimensions of 64, 128 and 256 run on the tensor
 // cores (paged_attention_mma.cuh); what follows here serves all others, and
-// unaligned tensors. It numbers the visible tokens 0, 1, ... without the gap that a
+// unaligned tensors, at the price that one CTA reads a query head's whole sequence (64
+// sequences of up to 4000 tokens, INT8, 32 query and 8 key heads: 2.0 ms with 80 or 96
+// channels against 64 us with 128 on the tensor cores). It numbers the visible tokens 0, 1, ... without the gap that a
 // window leaves behind the first tokens.
 #include <cmath>
 

@@ -53,8 +53,9 @@
 //
 // Bound by reading the cache: one sequence of 131072 tokens, bf16, 8 key heads takes
 // 88 us against 82 at the copy rate (6.1 TB/s); 64 ragged sequences of up to 8192,
-// INT8, 108 against 81 (opening the next item costs a CTA about 2 us each time,
-// and the start 5); 200 of up to 8000, INT8, 297 against 259; one of 127 tokens takes 5, nearly all of it latency.
+// INT8, 108.5 against 81 (opening the next item costs a CTA about 2 us each time,
+// and the start 5; DRAM at 59 % of its peak, issue slots at 38 %, tensor pipe at 16 %); 200
+// of up to 8000, INT8, 301 against 259; one of 127 tokens takes 5, nearly all of it latency.
 #pragma once
 
 #include <cuda.h>
@@ -1047,8 +1048,8 @@ constexpr int kPagedJoinThreads = 512;
 // per border between two ranges, and those inside an item share its heads. A head
 // takes D / 4 threads, each up to kBatch parts whose loads are all on their way
 // at once; of an item with more parts, several such rows, joined through shared memory.
-// It adds 3 us to the main kernel, most of them two trips to L2 (1 x 131072 bf16: 87.6 us
-// in all, 83.9 without it; 90.9 with one border doing all heads, a part after the
+// It adds 3 us to the main kernel, most of them two trips to L2 (1 x 131072 bf16: 88 us
+// in all, 84 without it; 91 with one border doing all heads, a part after the
 // other; 89 with kBatch 2, and 88 with 8, whose registers delay the CTAs' start).
 template <typename T, typename C, int D, int HT>
 __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel(const PagedArgs a) {

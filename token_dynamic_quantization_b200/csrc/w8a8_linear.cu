@@ -13,7 +13,8 @@
 namespace dq {
 
 // Any shape and alignment: one output per thread, integer dot product on CUDA
-// cores.
+// cores, byte by byte (1 x 4096 x 1000: 52 us, 512 x 1024 x 1000: 684; with k = 1008 the
+// latter takes 9 on the tensor cores).
 template <int ACT>
 __global__ void __launch_bounds__(256) w8a8_linear_generic_kernel(const LinearArgs a) {
   pdl_launch_dependents();

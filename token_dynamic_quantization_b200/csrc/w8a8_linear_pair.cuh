@@ -16,8 +16,9 @@
 //   warps 2-9   epilogue of the CTA's 128 rows, two warps to a TMEM quarter; the
 //               int32 accumulator is double-buffered in TMEM (2 x 256 columns), so
 //               it overlaps the next tile's MMAs
-// Bound by the tensor cores: 4096^3 with bias, GELU and residual takes 66 us, 41 of
-// them the products at twice the bf16 rate, about 8 the residual, and the rest the
+// 4096^3 with bias, GELU and residual takes 66 us, 41 of them the products at twice the
+// bf16 rate (the tensor pipe is active for half of a launch by itself, DRAM at 12 % of its
+// peak), about 8 the residual, and the rest the
 // start (7) and the last tiles' epilogue; without any of the three it takes 56, and
 // 9472 x 4096 x 8192 runs at 3.2 POP/s.
 // Every wait is bounded; after one has run out the CTA's remaining tiles become NaN.
