@@ -88,10 +88,10 @@ def test_one_large_scale_of_little_weight(dq, lengths, dim, log2_weight, log2_ra
     assert torch.equal(call(dq, s), out)
 
 
-@pytest.mark.parametrize("size", [1e-35, 1e-20, 1e31, 1e33, 1e36])
-@pytest.mark.parametrize("lengths,dim", SHAPES[:6])
+@pytest.mark.parametrize("size", [1e-35, 1e-20, 1e31, 1e33, 1e36, 6e37])
+@pytest.mark.parametrize("lengths,dim", [*SHAPES[:6], ([700], 80), ([333, 1, 20], 7)])
 def test_scales_over_the_whole_range(dq, lengths, dim, size):
-    """Scales from the end of binary32's range to that of bf16 outputs (a scale of 1e35 stands for values of 1e37)."""
+    """Scales from the end of binary32's range to that of bf16 outputs (6e37: values up to 3e38)."""
     s = make(lengths, 8, 2, dim, BF16, I8, 16, seed=33)
     s["v_scale"] *= size
     out = call(dq, s)

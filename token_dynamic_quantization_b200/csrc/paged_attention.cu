@@ -35,7 +35,7 @@ template <typename T, typename C>
 __global__ void __launch_bounds__(kPagedGenericWarps * 32) paged_attention_generic_kernel(const PagedArgs a) {
   constexpr bool kCodes = sizeof(C) == 1;
   constexpr int kChan = DQ_MAX_HEAD_DIM / 32;
-  __shared__ float s_m[kPagedGenericWarps], s_l[kPagedGenericWarps];
+  __shared__ float s_m[kPagedGenericWarps], s_l[kPagedGenericWarps], s_size[kPagedGenericWarps];
   __shared__ float s_o[kPagedGenericWarps][DQ_MAX_HEAD_DIM];
   pdl_launch_dependents();
   pdl_wait_primary();
@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(kPagedGenericWarps * 32) paged_attention_gener
     o[i] = 0.0f;
   }
   float m = -INFINITY, l = 0.0f;
+  float shrink = 1.0f;  // o is this much smaller: beside value scales past 2^64 it could overflow where the result does not
   for (int64_t i = warp; i < vis.count; i += kPagedGenericWarps) {
     const int64_t j = i < vis.first ? i : i + vis.skip;
     const int64_t p = j / a.page_size;
@@ -81,7 +82,16 @@ __global__ void __launch_bounds__(kPagedGenericWarps * 32) paged_attention_gener
     const float keep = m == next ? 1.0f : exp2f(m - next);
     const float w = s == -INFINITY ? 0.0f : exp2f(s - next);
     l = fmaf(l, keep, w);
-    const float wv = kCodes ? w * a.v_scale[row] : w;
+    float wv = w;
+    if (kCodes) {
+      wv = w * a.v_scale[row] * shrink;
+      if (fabsf(wv) > 0x1p64f) {
+        shrink = 0x1p-64f;
+        wv *= 0x1p-64f;
+#pragma unroll
+        for (int e = 0; e < kChan; ++e) o[e] *= 0x1p-64f;
+      }
+    }
 #pragma unroll
     for (int e = 0; e < kChan; ++e) {
       const int c = lane + 32 * e;
@@ -92,6 +102,7 @@ __global__ void __launch_bounds__(kPagedGenericWarps * 32) paged_attention_gener
   if (lane == 0) {
     s_m[warp] = m;
     s_l[warp] = l;
+    s_size[warp] = 1.0f / shrink;
   }
 #pragma unroll
   for (int i = 0; i < kChan; ++i) s_o[warp][lane + 32 * i] = o[i];
@@ -106,8 +117,8 @@ __global__ void __launch_bounds__(kPagedGenericWarps * 32) paged_attention_gener
   const bool empty = vis.count == 0;
   for (int c = threadIdx.x; c < a.head_dim; c += kPagedGenericWarps * 32) {
     float sum = 0.0f;
-    for (int w = 0; w < kPagedGenericWarps; ++w) sum = fmaf(s_o[w][c], f[w], sum);
-    const float r = empty ? 0.0f : sum / total;
+    for (int w = 0; w < kPagedGenericWarps; ++w) sum = fmaf(s_o[w][c] * (f[w] / total), s_size[w], sum);
+    const float r = empty ? 0.0f : sum;
     static_cast<T*>(a.out)[at * a.head_dim + c] = static_cast<T>(r);
   }
   if (threadIdx.x == 0 && a.lse != nullptr) a.lse[at] = empty ? -INFINITY : (top + log2f(total)) * kLn2;
