@@ -107,3 +107,17 @@ def test_scales_of_every_size_at_once(dq, dtype, dim, group):
     g = torch.Generator(device="cuda").manual_seed(35)
     s["v_scale"] *= torch.exp2(-60 * torch.rand(s["v_scale"].shape, generator=g, device="cuda"))
     check(s, call(dq, s))
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e34, 6e37])
+@pytest.mark.parametrize("lengths,dim", [([700], 128), ([9000, 40], 128), ([60] * 120, 64), ([300], 256)])
+def test_bf16_caches_of_any_size(dq, lengths, dim, size):
+    """Values of one sign near the end of bf16's range: their sums before the division would overflow binary32."""
+    from test_paged_attention_gpu import verify
+
+    s = make(lengths, 8, 2, dim, BF16, BF16, 16, seed=36)
+    s["v_cache"] = (s["v_cache"].float().abs() * size).to(BF16)
+    lse = torch.empty(len(lengths), 8, device="cuda")
+    out = call(dq, s, lse=lse)
+    assert out.isfinite().all()
+    verify(s, out, lse)

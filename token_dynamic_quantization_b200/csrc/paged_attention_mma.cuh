@@ -37,7 +37,7 @@
 //
 // The running maximum moves only when a score exceeds it by 8 (in log2), or beside
 // codes a weight times its scale may exceed f16's range: weights then stay below 2^(8 +
-// kLift) and the rescaling of O is rare. kLift raises the weights in f16 so that
+// kLift) and the rescaling of O is rare. In f16 kLift raises the weights so that
 // those down to 2^-30 of the largest count.
 //
 // What a warp or a CTA leaves for others to join is its own quotient O / sum beside
@@ -70,7 +70,17 @@
 namespace dq {
 
 constexpr float kSlack = 8.0f;  // log2 by which a score may exceed the running maximum
-constexpr float kLift = 6.0f;   // log2 of the weight at the running maximum
+// log2 of the weight at the running maximum: in f16 it raises the small ones above the type's
+// smallest steps; in bf16, whose range is that of the sums, it keeps those of values up to the
+// type's largest from overflowing before they are divided.
+constexpr int kLiftF16 = 6, kLiftBf16 = -16;
+template <typename T, typename C>
+constexpr float kLift = sizeof(C) == 2 && __is_same(T, __nv_bfloat16) ? kLiftBf16 : kLiftF16;
+// log2 of a sum of such weights, without the lift (which is exact as a factor)
+template <typename T, typename C>
+__device__ __forceinline__ float log2_weights(float sum) {
+  return log2f(sum * (sizeof(C) == 2 && __is_same(T, __nv_bfloat16) ? 0x1p16f : 0x1p-6f));
+}
 constexpr uint32_t kRowHidden = 0xFFFFFFFFu, kRowBad = 0xFFFFFFFEu;  // row numbers outside every cache
 
 // W: warps of a CTA, which share an item's tiles.
@@ -326,6 +336,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
   constexpr bool kCodes = Shape::kCodes;
   constexpr bool kBf16 = !kCodes && sizeof(T) == 2 && __is_same(T, __nv_bfloat16);
   // a weight as two operands of 16 bits; one of f16 does beside codes where the output is bf16
+  constexpr float kLift = dq::kLift<T, C>;
   constexpr bool kTwoParts = !kCodes || __is_same(T, __half);
   constexpr int TT = Shape::kTokens, MT = TT / 16, kHeads = Shape::kHeads;
   constexpr int kElem = sizeof(C);
@@ -1026,7 +1037,7 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
         // no weight at all, though tokens are visible: 0 / 0
         store_row4(static_cast<T*>(a.out) + at * D + c, sum, total == 0.0f && !empty ? NAN : 1.0f);
         if (a.lse != nullptr && c == 0)
-          a.lse[at] = empty ? -INFINITY : ((top == -INFINITY ? 0.0f : top) - kLift + log2f(total)) * kLn2;
+          a.lse[at] = empty ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2_weights<T, C>(total)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(part + h * D + c) = sum;
         if (c == 0) {
@@ -1140,7 +1151,7 @@ __global__ void __launch_bounds__(kPagedJoinThreads) paged_attention_join_kernel
   if (split == 0) {
     const int64_t at = cut.seq * a.q_heads + kvh * a.group + set * kHeads + h;
     store_row4(static_cast<T*>(a.out) + at * D + 4 * vec, sum, sum_l == 0.0f ? NAN : 1.0f);
-    if (vec == 0 && a.lse != nullptr) a.lse[at] = ((top == -INFINITY ? 0.0f : top) - kLift + log2f(sum_l)) * kLn2;
+    if (vec == 0 && a.lse != nullptr) a.lse[at] = ((top == -INFINITY ? 0.0f : top) + log2_weights<T, C>(sum_l)) * kLn2;
   }
 }
 
