@@ -640,8 +640,6 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
     // the power of two that takes the head's largest weight times value scale so far
     // into [1, 2)
     float v_mul[HT][2];
-    // its reciprocal
-    const auto v_size = [&](int ht, int c) { return __uint_as_float((254u << 23) - __float_as_uint(v_mul[ht][c])); };
 #pragma unroll
     for (int ht = 0; ht < HT; ++ht) {
       v_mul[ht][0] = v_mul[ht][1] = 0x1p126f;
@@ -651,6 +649,9 @@ __global__ void __launch_bounds__(32 * W, (PagedShape<C, D, HT, W>::kCtas))
 #pragma unroll
       for (int i = 0; i < KS; ++i) o[ht][i][0] = o[ht][i][1] = o[ht][i][2] = o[ht][i][3] = 0.0f;
     }
+
+    // v_mul's reciprocal, a power of two as well
+    const auto v_size = [&](int ht, int c) { return __uint_as_float((254u << 23) - __float_as_uint(v_mul[ht][c])); };
 
     // groups whose tokens are all visible
     const int inside_first = vis.first_groups == 0 && (vis.start & 15) == 0 ? 0 : vis.first_groups + ((vis.start & 15) != 0 ? 1 : 0);
